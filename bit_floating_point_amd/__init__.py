@@ -17,10 +17,14 @@ from . import _lib as L
 from ._lib import (FP4Error, FP4_BF16, FP4_F16, FP4_F32, FP4_PACKED, FP4_REDUCE_COLUMN,
                    FP4_REDUCE_ROW_GROUP, FP4_REDUCE_TENSOR, FP4_SCALE_GROUP, FP4_SCALE_ROW,
                    FP4_SCALE_TENSOR)
+from .layer import (Routing, fp4_gemm_block, fp4_gemm_experts, fp4_quantize_block, fp4_rmsnorm_quant, fp4_route,
+                    fp4_swiglu_quant)
 
 __all__ = ["FP4Error", "grid_minifloat", "grid_lut", "grid_nf4", "grid_two_mode", "nf4_values", "set_split_limit", "gran", "fp4_calibrate", "fp4_quantize_pack",
            "fp4_dequantize", "fp4_preshift_weights", "fp4_search_format", "fp4_search_format_static", "fp4_gemm",
-           "fp4_gemm_swiglu_quant", "fp4_search_activations", "search_results_host", "E2M1", "E1M2", "E3M0"]
+           "fp4_gemm_swiglu_quant", "fp4_search_activations", "search_results_host", "E2M1", "E1M2", "E3M0",
+           "fp4_rmsnorm_quant", "fp4_swiglu_quant", "fp4_quantize_block", "fp4_gemm_block", "fp4_route", "fp4_gemm_experts",
+           "Routing"]
 
 
 def grid_minifloat(e: int, m: int) -> L.fp4_grid:

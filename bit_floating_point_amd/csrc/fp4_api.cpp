@@ -9,6 +9,7 @@
 
 #include "../../include/fp4.h"
 #include "fp4_internal.h"
+#include "layer_internal.h"
 
 using namespace fp4;
 
@@ -137,6 +138,22 @@ int64_t units_of(const fp4_gran& g, int64_t rows, int64_t cols) {
 }
 
 }  // namespace
+
+// the error message, grid tables and HIP status for layer_api.cpp
+namespace fp4 {
+
+fp4_status report(fp4_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+fp4_status report_ok() { return ok(); }
+fp4_status report_hip(hipError_t e, const char* what) { return hip_status(e, what); }
+fp4_status grid_table(const fp4_grid& g, QGrid* q) { return make_grid(g, q); }
+
+}  // namespace fp4
 
 extern "C" {
 
