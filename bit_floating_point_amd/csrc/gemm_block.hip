@@ -30,12 +30,325 @@ __device__ __forceinline__ i32x8 load32(const uint8_t* row, int64_t k, int64_t K
     return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
 }
 
+// four consecutive columns of a row, of which those below N are written
+__device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d);
+
 __device__ __forceinline__ void store_y(const BlockGemmParams& p, int64_t row, int64_t col, float v) {
     if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[row * p.ldy + col] = (__bf16)v;
     else reinterpret_cast<float*>(p.y)[row * p.ldy + col] = v;
 }
 
+__device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d) {
+    if (p.y_vec && col + 4 <= p.N) {
+        const int64_t at = row * p.ldy + col;
+        if (p.y_bf16) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p.y) + at) = bf16x4{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
+        } else {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.y) + at) = make_float4(a, b, c, d);
+        }
+    } else {
+        if (col < p.N) store_y(p, row, col, a);
+        if (col + 1 < p.N) store_y(p, row, col + 1, b);
+        if (col + 2 < p.N) store_y(p, row, col + 2, c);
+        if (col + 3 < p.N) store_y(p, row, col + 3, d);
+    }
+}
+
 }  // namespace
+
+
+// ---- tile kernel -----------------------------------------------------------------------
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// Direct-to-LDS loads, 16 or 4 bytes per lane: lane l writes LDS bytes base + off + size l
+// from the buffer at voff + soff (nothing, that is zeros, where voff is past the buffer).
+__device__ __forceinline__ void lds_load16(i32x4v rsrc, uint32_t voff, uint32_t soff, uint32_t base, uint32_t off) {
+    asm volatile("s_add_u32 m0, %2, %3\n\tbuffer_load_dwordx4 %0, %4, %1 offen lds"
+                 :
+                 : "v"(voff), "s"(soff), "s"(base), "s"(off), "s"(rsrc)
+                 : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void lds_load4(i32x4v rsrc, uint32_t voff, uint32_t soff, uint32_t base, uint32_t off) {
+    asm volatile("s_add_u32 m0, %2, %3\n\tbuffer_load_dword %0, %4, %1 offen lds"
+                 :
+                 : "v"(voff), "s"(soff), "s"(base), "s"(off), "s"(rsrc)
+                 : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+// All of this wavefront's direct-to-LDS loads have landed and its LDS reads returned; then
+// the workgroup barrier.
+__device__ __forceinline__ void step_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+// The m-tile and column block of a workgroup, in experts' mode its expert and slots.
+struct Tile {
+    int64_t e, lo, hi, m0;  // expert; its range of the list (dense: [0, M)); first row of the tile
+    int n;                  // column block
+    bool live;
+};
+
+// Workgroups go to the 8 XCDs in turn: XCD x takes the x-th eighth of the tiles, so that the
+// tiles that share operands meet in one L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t ntiles) {
+    const int64_t full = ntiles / 8 * 8;
+    return b < full ? (b % 8) * (full / 8) + b / 8 : b;
+}
+
+template <int BM>
+__device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n) {
+    const int lane = threadIdx.x & 63;
+    auto range = [&](int e, int& lo, int& hi) {
+        lo = hi = 0;
+        if (e < p.experts) {
+            lo = max(p.offsets[e], 0);
+            hi = (int)min((int64_t)p.offsets[e + 1], p.M);
+        }
+        return hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    };
+    int total = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+        int lo, hi, c = range(e0 + lane, lo, hi);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) c += __shfl_xor(c, o, 64);
+        total += c;
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    Tile t{};
+    const int64_t ntiles = (int64_t)total * grid_n;
+    if ((int64_t)blockIdx.x >= ntiles) return t;
+    const int64_t at = xcd_order(blockIdx.x, ntiles);
+    const int want = (int)(at / grid_n);
+    int before = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+        int lo, hi;
+        const int c = range(e0 + lane, lo, hi);
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(s, o, 64);
+            if (lane >= o) s += u;
+        }
+        const uint64_t hit = __ballot(before + s > want);
+        if (hit) {
+            const int l = __ffsll((unsigned long long)hit) - 1;
+            const int first = before + __shfl(s - c, l, 64), mt = __shfl(c, l, 64);
+            const int r = __builtin_amdgcn_readfirstlane((int)(at - (int64_t)first * grid_n));
+            const int m = __builtin_amdgcn_readfirstlane(mt), from = __builtin_amdgcn_readfirstlane(__shfl(lo, l, 64));
+            t.e = __builtin_amdgcn_readfirstlane(e0 + l);
+            t.lo = from;
+            t.hi = __builtin_amdgcn_readfirstlane(__shfl(hi, l, 64));
+            t.m0 = from + (int64_t)(r % m) * BM;
+            t.n = r / m;
+            t.live = true;
+            return t;
+        }
+        before += __shfl(s, 63, 64);
+    }
+    return t;
+}
+
+// A workgroup of WM x WN wavefronts computes BM x BN outputs, each wavefront MT x NT
+// results of 32 x 32 (its m-tiles every WM-th of the tile's, so that a short tile's rows
+// spread over the wavefronts).
+template <int FW, int FA, int BM, int BN, int WM, int WN, bool EXP>
+__global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemmParams p, int grid_m, int grid_n) {
+    constexpr int NW = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
+    constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
+    // scales: chunks of 8 blocks of K, BM rows (and the column blocks of W) of 8 values
+    constexpr int CH = BM * 32 + 256 * (NW - BM / 64);
+    constexpr int LA = SA / 1024 / NW, LB = SB / 1024 / NW;
+    static_assert(BM / 64 < NW, "one wavefront per 64 scales of A, one for those of W");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + 2 * CH];
+    __shared__ uint32_t scale_row[BM + 64];  // byte offset of the scales of each row, then of each column block
+    uint8_t* const smem_s = smem + 2 * STAGE;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int r32 = lane & 31, hk = lane >> 5;
+
+    Tile tile;
+    if constexpr (EXP) {
+        tile = expert_tile<BM>(p, grid_n);
+        if (!tile.live) return;
+    } else {
+        // panels of four row blocks, column by column: the tiles that an XCD computes at
+        // one time form a compact block
+        const int64_t t = xcd_order(blockIdx.x, (int64_t)grid_m * grid_n);
+        constexpr int P = 4;
+        const int panel = (int)(t / ((int64_t)P * grid_n)), rows = min(P, grid_m - panel * P);
+        const int r = (int)(t - (int64_t)panel * P * grid_n);
+        tile.e = 0;
+        tile.lo = 0;
+        tile.hi = p.M;
+        tile.m0 = (int64_t)(panel * P + r % rows) * BM;
+        tile.n = r / rows;
+    }
+    const int64_t n0 = (int64_t)tile.n * BN;
+    const int kb = (int)((p.K + 127) / 128), K = (int)p.K;
+    // output row and source row of the tile's row r, or -1
+    auto rows_of = [&](int r, int64_t& src) -> int64_t {
+        const int64_t m = tile.m0 + r;
+        if (m >= tile.hi) return -1;
+        if constexpr (!EXP) {
+            src = r;  // from the tile's first row
+            return m;
+        } else {
+            const int64_t s = p.slot_list[m];
+            if (s < 0 || s >= p.M) return -1;
+            src = s / p.slots_per_row;
+            return s;
+        }
+    };
+
+    // loads: LDS row r holds 8 pieces of 16 bytes, piece s at position s ^ (r / 2 % 8), so
+    // that the 16 rows a fragment read serves at once lie in different banks
+    const int64_t a_rows = EXP ? (p.M + p.slots_per_row - 1) / p.slots_per_row : min((int64_t)BM, p.M - tile.m0);
+    const i32x4v rsA = buf_words(EXP ? p.a : p.a + tile.m0 * p.lda, a_rows * p.lda);
+    const i32x4v rsB = buf_words(p.w + tile.e * p.stride_w + n0 * p.ldw, min((int64_t)BN, p.N - n0) * p.ldw);
+    // scales: wavefront w < BM / 64 those of 64 rows of A, the next one those of W's blocks
+    const int64_t nb0 = n0 / 128, nbs = min((int64_t)((BN + 127) / 128), (p.N + 127) / 128 - nb0);
+    const bool of_a = wave < BM / 64;
+    const i32x4v rsS = of_a ? buf_words(EXP ? p.a_scales : p.a_scales + tile.m0 * p.lda_s, a_rows * p.lda_s * 4)
+                            : buf_words(p.w_scales + tile.e * p.stride_ws + nb0 * p.ldw_s, nbs * p.ldw_s * 4);
+    const int seg = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
+    // dense operands: one offset per lane, the later pieces by the scalar offset (the range
+    // check includes it, so rows past the operand read zeros)
+    uint32_t offA[EXP ? LA : 1], offB;
+    const int r8 = wave * 8 + (lane >> 3);
+    if constexpr (EXP) {
+#pragma unroll
+        for (int i = 0; i < LA; i++) {
+            int64_t src = 0;
+            const int64_t out = rows_of(NW * 8 * i + r8, src);
+            offA[i] = out < 0 ? kOOB : (uint32_t)(src * p.lda + seg * 16);
+        }
+    } else {
+        offA[0] = (uint32_t)(r8 * (int)p.lda + seg * 16);
+    }
+    offB = (uint32_t)(r8 * (int)p.ldw + seg * 16);
+    const uint32_t stepA = (uint32_t)(NW * 8 * (int)p.lda), stepB = (uint32_t)(NW * 8 * (int)p.ldw);
+    for (int r = threadIdx.x; r < BM + 64; r += 64 * NW) {
+        int64_t src = r - BM;
+        if (r < BM) scale_row[r] = rows_of(r, src) < 0 ? kOOB : (uint32_t)(src * p.lda_s * 4);
+        else scale_row[r] = src < nbs ? (uint32_t)(src * p.ldw_s * 4) : kOOB;
+    }
+    __syncthreads();
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+    const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
+    const uint32_t lds_scale = __builtin_amdgcn_readfirstlane(lds + 2 * STAGE + wave * 256);
+    auto load = [&](int b, uint32_t stage) {
+        // pieces past K read zeros (and so do whole stages past it: the loop has no branch)
+        const uint32_t k = (uint32_t)(b * 128);
+        const uint32_t dead = (int)k + seg * 16 < K ? 0u : kOOB;
+#pragma unroll
+        for (int i = 0; i < LA; i++) {
+            if constexpr (EXP) lds_load16(rsA, offA[i] |= dead, k, lds_wave, stage + NW * i * 1024);
+            else lds_load16(rsA, offA[0] |= dead, k + i * stepA, lds_wave, stage + NW * i * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < LB; i++) lds_load16(rsB, offB |= dead, k + i * stepB, lds_wave, stage + SA + NW * i * 1024);
+    };
+    // Part c (of 8) of the scales' chunk q (blocks 8 q .. 8 q + 7): 8 values of BM / 8 rows,
+    // and with every part those of W.  A load instruction then touches 8 lines, not 64.
+    // Block k of row r sits at position k ^ (r / 8 % 8): the reads of 32 rows fall into
+    // different banks.
+    auto load_scales = [&](int q, int c) {
+        const int group = BM / 64 * c + wave;  // of 8 rows
+        const uint32_t row = scale_row[(of_a ? 8 * group : BM + 8 * (wave - BM / 64)) + (lane >> 3)];
+        const int k = q * 8 + ((lane & 7) ^ (of_a ? group & 7 : 0));
+        lds_load4(rsS, (row + (uint32_t)k * 4) | (k < kb ? 0u : kOOB), 0, lds_scale,
+                  (uint32_t)(q & 1) * CH + (of_a ? BM * 4 * c : BM * 28));
+    };
+
+    // fragment h (64 codes) of LDS row `row`: pieces 4 h + 2 hk and the next
+    const int x = (r32 >> 1) & 7;
+    auto frag = [&](const uint8_t* rows, int row, int h) -> i32x8 {
+        const uint8_t* q = rows + (row + r32) * 128;
+        const uint4 u = *reinterpret_cast<const uint4*>(q + (((4 * h + 2 * hk) ^ x) << 4));
+        const uint4 v = *reinterpret_cast<const uint4*>(q + (((4 * h + 2 * hk + 1) ^ x) << 4));
+        return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+    };
+
+    f32x16 t[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) t[i][j] = f32x16{};
+
+    load(0, 0);
+#pragma unroll
+    for (int c = 0; c < 8; c++) load_scales(0, c);
+    step_barrier();
+    load(1, STAGE);
+    load_scales(1, 0);
+    for (int b = 0; b < kb; b++) {
+        const uint32_t cur = (uint32_t)(b & 1) * STAGE;
+        const uint8_t* sa = smem + cur;
+        const uint8_t* sb = sa + SA;
+        const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) & 1) * CH);
+        const int c8 = b & 7;
+        const float sw = sc[BM * 8 + (wn * NT * 32) / 128 * 8 + c8];
+        i32x8 w[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) w[j][h] = frag(sb, (wn * NT + j) * 32, h);
+        i32x8 a[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) a[h] = frag(sa, wm * 32, h);
+        f32x16 c[NT];
+        float s[MT];
+#pragma unroll
+        for (int i = 0; i < MT; i++) s[i] = sc[((i * WM + wm) * 32 + r32) * 8 + (c8 ^ (((i * WM + wm) * 4 + (r32 >> 3)) & 7))] * sw;
+        // m-tile i: the first halves of its NT block sums, then the second; a sum is folded
+        // into t while the matrix cores work on the next one
+        auto fold = [&](int i, int j) {
+#pragma unroll
+            for (int v = 0; v < 16; v++) t[i][j][v] = __builtin_fmaf(c[j][v], s[i], t[i][j][v]);
+        };
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            if (i + 1 == MT) {
+                // every fragment of this stage is read (by all wavefronts, past the barrier)
+                // and the next stage's loads, issued one step ago, have landed
+                step_barrier();
+                load(b + 2, cur);
+                load_scales(((b + 1) >> 3) + 1, (b + 1) & 7);  // landed a step before its chunk's first use
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                if (i > 0 && j + 1 == NT) fold(i - 1, NT - 1);
+                c[j] = mfma64<FW, FA>(w[j][0], a[0], f32x16{});
+            }
+            if (i + 1 < MT) a[0] = frag(sa, ((i + 1) * WM + wm) * 32, 0);
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                c[j] = mfma64<FW, FA>(w[j][1], a[1], c[j]);
+                if (j > 0) fold(i, j - 1);
+            }
+            if (i + 1 < MT) a[1] = frag(sa, ((i + 1) * WM + wm) * 32, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        fold(MT - 1, NT - 1);
+    }
+    step_barrier();  // no load into LDS outlives the workgroup
+
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+        int64_t src = 0;
+        const int64_t out = rows_of((i * WM + wm) * 32 + r32, src);
+        if (out < 0) continue;
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const int64_t col = n0 + (wn * NT + j) * 32 + 8 * g + 4 * hk;
+                store_y4(p, out, col, t[i][j][4 * g], t[i][j][4 * g + 1], t[i][j][4 * g + 2], t[i][j][4 * g + 3]);
+            }
+    }
+}
 
 // 64 x 64 tile, four wavefronts of 32 x 32; fragments straight from memory.
 template <int FW, int FA>
@@ -90,9 +403,32 @@ static hipError_t launch_direct(const BlockGemmParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_gemm_block(const BlockGemmParams& p, hipStream_t s) {
-    if (p.fw == 0) return p.fa == 0 ? launch_direct<0, 0>(p, s) : launch_direct<0, 1>(p, s);
-    return p.fa == 0 ? launch_direct<1, 0>(p, s) : launch_direct<1, 1>(p, s);
+template <int FW, int FA, int BM, int BN, int WM, int WN>
+static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
+    const int64_t grid_n = (p.N + BN - 1) / BN;
+    if (p.experts) {
+        const int64_t most = p.M / BM + (p.experts < p.M ? p.experts : p.M);  // m-tiles, however the slots fall
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, true><<<(unsigned)(most * grid_n), 64 * WM * WN, 0, s>>>(p, 0, (int)grid_n);
+    } else {
+        const int64_t grid_m = (p.M + BM - 1) / BM;
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, false>
+            <<<(unsigned)(grid_m * grid_n), 64 * WM * WN, 0, s>>>(p, (int)grid_m, (int)grid_n);
+    }
+    return hipGetLastError();
+}
+
+template <int FW, int FA>
+static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
+    const int64_t rows = p.experts ? p.M / p.experts : p.M;
+    if (rows >= 256) return launch_tiles<FW, FA, 256, 256, 2, 4>(p, s);
+    return launch_direct<FW, FA>(p, s);
+}
+
+hipError_t launch_gemm_block(const BlockGemmParams& in, hipStream_t s) {
+    BlockGemmParams p = in;
+    p.y_vec = p.ldy % 4 == 0;
+    if (p.fw == 0) return p.fa == 0 ? launch_formats<0, 0>(p, s) : launch_formats<0, 1>(p, s);
+    return p.fa == 0 ? launch_formats<1, 0>(p, s) : launch_formats<1, 1>(p, s);
 }
 
 }  // namespace fp4

@@ -219,6 +219,7 @@ fp4_status fp4_gemm_block(const fp4_gemm_block_desc* d, void* stream) {
     if ((st = product_output(d->y, d->ldy, d->N, d->y_dtype))) return st;
     if (d->lda_s < blocks_of(d->K) || d->ldw_s < blocks_of(d->K))
         return report(FP4_ERR_INVALID_ARG, "leading dimension of scales below ceil(K / 128)");
+    if (d->lda_s > (1 << 20) || d->ldw_s > (1 << 20)) return report(FP4_ERR_UNSUPPORTED, "rows of scales must be shorter than 4 MiB");
     if (d->M == 0 || d->N == 0) return report_ok();
     if (!d->a || !d->a_scales || !d->w || !d->w_scales || !d->y) return report(FP4_ERR_INVALID_ARG, "null pointer");
     if (!aligned(d->a_scales, 4) || !aligned(d->w_scales, 4)) return report(FP4_ERR_ALIGNMENT, "scales must be 4-byte aligned");
@@ -302,6 +303,7 @@ fp4_status fp4_gemm_experts(const fp4_gemm_experts_desc* d, void* stream) {
     if ((st = code_operand("a", d->a, d->lda, d->K, d->a_grid, &p.fa))) return st;
     if ((st = code_operand("w", d->w, d->ldw, d->K, d->w_grid, &p.fw))) return st;
     if ((st = product_output(d->y, d->ldy, d->N, d->y_dtype))) return st;
+    if (d->lda_s > (1 << 20)) return report(FP4_ERR_UNSUPPORTED, "rows of scales must be shorter than 4 MiB");
     if (d->lda_s < blocks_of(d->K)) return report(FP4_ERR_INVALID_ARG, "leading dimension of scales below ceil(K / 128)");
     if (d->stride_w < 0) return report(FP4_ERR_INVALID_ARG, "bad stride between experts");
     if (d->stride_w % 16 != 0) return report(FP4_ERR_ALIGNMENT, "experts must be a multiple of 16 bytes apart");
