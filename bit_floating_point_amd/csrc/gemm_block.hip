@@ -7,6 +7,8 @@
 // The weight tile is the instruction's first operand, so a lane of a 32 x 32 result holds
 // 16 columns n of one row m: both scales are one value per lane and block, and four
 // consecutive columns leave in one store.
+#include <cmath>
+
 #include "fp4_device.h"
 #include "layer_internal.h"
 
@@ -15,6 +17,7 @@ namespace fp4 {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int FW, int FA>
@@ -22,12 +25,9 @@ __device__ __forceinline__ f32x16 mfma64(i32x8 w, i32x8 a, f32x16 c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, FW, FA, 0, 127, 0, 127);
 }
 
-// 32 codes of a row at k .. k + 31, zeros past K (a multiple of 16); `row` null: zeros
-__device__ __forceinline__ i32x8 load32(const uint8_t* row, int64_t k, int64_t K) {
-    uint4 u = make_uint4(0, 0, 0, 0), v = u;
-    if (row && k < K) u = *reinterpret_cast<const uint4*>(row + k);
-    if (row && k + 16 < K) v = *reinterpret_cast<const uint4*>(row + k + 16);
-    return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+template <int FW, int FA>
+__device__ __forceinline__ f32x4 mfma128(i32x8 w, i32x8 a, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, FW, FA, 0, 127, 0, 127);
 }
 
 // four consecutive columns of a row, of which those below N are written
@@ -76,9 +76,12 @@ __device__ __forceinline__ void lds_load4(i32x4v rsrc, uint32_t voff, uint32_t s
                  : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
-// All of this wavefront's direct-to-LDS loads have landed and its LDS reads returned; then
-// the workgroup barrier.
-__device__ __forceinline__ void step_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+// At most N of this wavefront's direct-to-LDS loads are in flight and its LDS reads have
+// returned; then the workgroup barrier.
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
 
 // The m-tile and column block of a workgroup, in experts' mode its expert and slots.
 struct Tile {
@@ -147,20 +150,21 @@ __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n
     return t;
 }
 
+// S stages of 128 codes of K are in LDS or on their way there.
 // A workgroup of WM x WN wavefronts computes BM x BN outputs, each wavefront MT x NT
 // results of 32 x 32 (its m-tiles every WM-th of the tile's, so that a short tile's rows
 // spread over the wavefronts).
-template <int FW, int FA, int BM, int BN, int WM, int WN, bool EXP>
-__global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemmParams p, int grid_m, int grid_n) {
+template <int FW, int FA, int BM, int BN, int WM, int WN, int S, bool EXP>
+__global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockGemmParams p, int grid_m, int grid_n) {
     constexpr int NW = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
     constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
     // scales: chunks of 8 blocks of K, BM rows (and the column blocks of W) of 8 values
-    constexpr int CH = BM * 32 + 256 * (NW - BM / 64);
+    constexpr int CH = BM * 32 + 256 * (NW - BM / 64), NCH = S > 2 ? 3 : 2;
     constexpr int LA = SA / 1024 / NW, LB = SB / 1024 / NW;
     static_assert(BM / 64 < NW, "one wavefront per 64 scales of A, one for those of W");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + 2 * CH];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + NCH * CH];
     __shared__ uint32_t scale_row[BM + 64];  // byte offset of the scales of each row, then of each column block
-    uint8_t* const smem_s = smem + 2 * STAGE;
+    uint8_t* const smem_s = smem + S * STAGE;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -236,16 +240,18 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
     __syncthreads();
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
     const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
-    const uint32_t lds_scale = __builtin_amdgcn_readfirstlane(lds + 2 * STAGE + wave * 256);
-    auto load = [&](int b, uint32_t stage) {
-        // pieces past K read zeros (and so do whole stages past it: the loop has no branch)
-        const uint32_t k = (uint32_t)(b * 128);
-        const uint32_t dead = (int)k + seg * 16 < K ? 0u : kOOB;
+    const uint32_t lds_scale = __builtin_amdgcn_readfirstlane(lds + S * STAGE + wave * 256);
+    // Pieces past K read zeros, and so do whole stages past it (the loop has no branch).
+    auto load_a = [&](int b, uint32_t stage) {
+        const uint32_t k = (uint32_t)(b * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
 #pragma unroll
         for (int i = 0; i < LA; i++) {
             if constexpr (EXP) lds_load16(rsA, offA[i] |= dead, k, lds_wave, stage + NW * i * 1024);
             else lds_load16(rsA, offA[0] |= dead, k + i * stepA, lds_wave, stage + NW * i * 1024);
         }
+    };
+    auto load_w = [&](int b, uint32_t stage) {
+        const uint32_t k = (uint32_t)(b * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
 #pragma unroll
         for (int i = 0; i < LB; i++) lds_load16(rsB, offB |= dead, k + i * stepB, lds_wave, stage + SA + NW * i * 1024);
     };
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
         const uint32_t row = scale_row[(of_a ? 8 * group : BM + 8 * (wave - BM / 64)) + (lane >> 3)];
         const int k = q * 8 + ((lane & 7) ^ (of_a ? group & 7 : 0));
         lds_load4(rsS, (row + (uint32_t)k * 4) | (k < kb ? 0u : kOOB), 0, lds_scale,
-                  (uint32_t)(q & 1) * CH + (of_a ? BM * 4 * c : BM * 28));
+                  (uint32_t)(q % NCH) * CH + (of_a ? BM * 4 * c : BM * 28));
     };
 
     // fragment h (64 codes) of LDS row `row`: pieces 4 h + 2 hk and the next
@@ -276,17 +282,28 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
 #pragma unroll
         for (int j = 0; j < NT; j++) t[i][j] = f32x16{};
 
-    load(0, 0);
+    // A step's loads: the stage S steps ahead, and a part of the scales' chunk that has landed
+    // before the chunk's first use.
+    constexpr int GROUP = LA + LB + 1;
+    auto load_rest = [&](int b, uint32_t stage) {
+        load_w(b + S, stage);
+        load_scales(((b + S - 1) >> 3) + 1, (b + S - 1) & 7);
+    };
 #pragma unroll
     for (int c = 0; c < 8; c++) load_scales(0, c);
-    step_barrier();
-    load(1, STAGE);
-    load_scales(1, 0);
+#pragma unroll
+    for (int q = 0; q < S - 1; q++) load_scales(1, q);
+#pragma unroll
+    for (int q = 0; q < S; q++) {
+        load_w(q, q * STAGE);
+        load_a(q, q * STAGE);
+    }
+    step_barrier<(S - 1) * (LA + LB)>();
+    uint32_t cur = 0;
     for (int b = 0; b < kb; b++) {
-        const uint32_t cur = (uint32_t)(b & 1) * STAGE;
         const uint8_t* sa = smem + cur;
         const uint8_t* sb = sa + SA;
-        const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) & 1) * CH);
+        const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) % NCH) * CH);
         const int c8 = b & 7;
         const float sw = sc[BM * 8 + (wn * NT * 32) / 128 * 8 + c8];
         i32x8 w[NT][2];
@@ -309,12 +326,22 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
         };
 #pragma unroll
         for (int i = 0; i < MT; i++) {
+            if (i == 1 && MT > 2) {
+                // every wavefront has read this stage's weights: those S steps on replace them
+                step_barrier<S * GROUP>();
+                load_rest(b, cur);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if (i + 1 == MT) {
                 // every fragment of this stage is read (by all wavefronts, past the barrier)
-                // and the next stage's loads, issued one step ago, have landed
-                step_barrier();
-                load(b + 2, cur);
-                load_scales(((b + 1) >> 3) + 1, (b + 1) & 7);  // landed a step before its chunk's first use
+                // and the next stage's loads have landed
+                if constexpr (MT > 2) {
+                    step_barrier<(S - 2) * GROUP + LB + 1>();
+                } else {
+                    step_barrier<(S - 2) * GROUP>();
+                    load_rest(b, cur);
+                }
+                load_a(b + S, cur);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -332,8 +359,9 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
             __builtin_amdgcn_sched_barrier(0);
         }
         fold(MT - 1, NT - 1);
+        cur = cur + STAGE == S * STAGE ? 0 : cur + STAGE;
     }
-    step_barrier();  // no load into LDS outlives the workgroup
+    step_barrier<0>();  // no load into LDS outlives the workgroup
 
 #pragma unroll
     for (int i = 0; i < MT; i++) {
@@ -350,78 +378,179 @@ __global__ void __launch_bounds__(64 * WM * WN) block_gemm_tile_kernel(BlockGemm
     }
 }
 
-// 64 x 64 tile, four wavefronts of 32 x 32; fragments straight from memory.
-template <int FW, int FA>
-__global__ void __launch_bounds__(256) block_gemm_direct_kernel(BlockGemmParams p) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r32 = lane & 31, hk = lane >> 5;
-    const int64_t e = p.experts ? blockIdx.z : 0;
-    int64_t lo = 0, hi = p.M;
-    if (p.experts) {
-        lo = p.offsets[e] < 0 ? 0 : p.offsets[e];
-        hi = p.offsets[e + 1] > p.M ? p.M : p.offsets[e + 1];
+// ---- few rows ----------------------------------------------------------------------------
+// Reading the weights is what the product costs.  A workgroup computes 16 MT rows of A by
+// 16 NT rows of W; its KS wavefronts take the blocks of K between them, each streaming its
+// operands straight into fragments, D blocks ahead, and the KS partial sums are added in
+// order through LDS.  The 16 x 16 x 128 instruction takes a whole block, so its result is
+// the block's sum.
+template <int FW, int FA, int MT, int NT, int KS, int D, bool EXP>
+__global__ void __launch_bounds__(64 * KS, 2) block_gemm_stream_kernel(BlockGemmParams p, int grid_m, int grid_n) {
+    constexpr int BM = 16 * MT, BN = 16 * NT;
+    __shared__ f32x4 part[KS][MT * NT][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+
+    Tile tile;
+    if constexpr (EXP) {
+        tile = expert_tile<BM>(p, grid_n);
+        if (!tile.live) return;
+    } else {
+        tile.e = 0;
+        tile.lo = 0;
+        tile.hi = p.M;
+        tile.m0 = (int64_t)(blockIdx.x % grid_m) * BM;
+        tile.n = blockIdx.x / grid_m;
     }
-    const int64_t n0 = (int64_t)blockIdx.x * 64 + (wave & 1) * 32;
-    const uint8_t* w = p.w + e * p.stride_w;
-    const float* ws = p.w_scales + e * p.stride_ws;
-    for (int64_t m0 = lo + (int64_t)blockIdx.y * 64 + (wave >> 1) * 32; m0 < hi; m0 += (int64_t)gridDim.y * 64) {
-        const int64_t m = m0 + r32, n = n0 + r32;
-        int64_t out = m, src = m;
-        if (m >= hi) {
-            out = -1;
-        } else if (p.experts) {
-            out = p.slot_list[m];
-            if (out < 0 || out >= p.M) out = -1;
-            src = out / p.slots_per_row;
-        }
-        const uint8_t* arow = out >= 0 ? p.a + src * p.lda : nullptr;
-        const uint8_t* wrow = n < p.N ? w + n * p.ldw : nullptr;
-        f32x16 t = {};
-        for (int64_t k = 0; k < p.K; k += 128) {
-            f32x16 c = {};
-            c = mfma64<FW, FA>(load32(wrow, k + 32 * hk, p.K), load32(arow, k + 32 * hk, p.K), c);
-            c = mfma64<FW, FA>(load32(wrow, k + 64 + 32 * hk, p.K), load32(arow, k + 64 + 32 * hk, p.K), c);
-            const float s = out >= 0 && n0 < p.N ? p.a_scales[src * p.lda_s + k / 128] * ws[n0 / 128 * p.ldw_s + k / 128] : 0.0f;
+    const int64_t n0 = (int64_t)tile.n * BN;
+    const int kb = (int)((p.K + 127) / 128), K = (int)p.K;
+    const int64_t a_rows = EXP ? (p.M + p.slots_per_row - 1) / p.slots_per_row : min((int64_t)BM, p.M - tile.m0);
+    const __amdgpu_buffer_rsrc_t rA = buf_make(EXP ? p.a : p.a + tile.m0 * p.lda, a_rows * p.lda);
+    const __amdgpu_buffer_rsrc_t rS = buf_make(EXP ? p.a_scales : p.a_scales + tile.m0 * p.lda_s, a_rows * p.lda_s * 4);
+    const __amdgpu_buffer_rsrc_t rW = buf_make(p.w + tile.e * p.stride_w + n0 * p.ldw, min((int64_t)BN, p.N - n0) * p.ldw);
+    const __amdgpu_buffer_rsrc_t rV = buf_make(p.w_scales + tile.e * p.stride_ws + n0 / 128 * p.ldw_s, (int64_t)kb * 4);
+    int64_t out[MT];
+    uint32_t offA[MT], offS[MT];
 #pragma unroll
-            for (int v = 0; v < 16; v++) t[v] = __builtin_fmaf(c[v], s, t[v]);
+    for (int i = 0; i < MT; i++) {
+        const int64_t m = tile.m0 + 16 * i + r16;
+        int64_t src = 16 * i + r16;
+        out[i] = m < tile.hi ? m : -1;
+        if constexpr (EXP) {
+            if (out[i] >= 0) out[i] = p.slot_list[m];
+            if (out[i] >= p.M) out[i] = -1;
+            src = out[i] / p.slots_per_row;
         }
-        if (out >= 0) {
+        offA[i] = out[i] < 0 ? kOOB : (uint32_t)(src * p.lda + 16 * g);
+        offS[i] = out[i] < 0 ? kOOB : (uint32_t)(src * p.lda_s * 4);
+    }
+    const uint32_t offW = (uint32_t)(r16 * (int)p.ldw + 16 * g);
+
+    struct Stage {
+        i32x8 w[NT], a[MT];
+        float sa[MT], sw;
+    } st[D];
+    // A lane's 32 codes of a block: pieces g and 4 + g of 16 (any assignment of codes to lanes
+    // that both operands share gives the block's sum; with this one the four lanes of a row
+    // read 64 contiguous bytes).
+    auto load32 = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, uint32_t d0, uint32_t d1) -> i32x8 {
+        const auto u = __builtin_amdgcn_raw_buffer_load_b128(r, off | d0, soff, 0);
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (off + 64) | d1, soff, 0);
+        return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+    };
+    const int per = (kb + KS - 1) / KS, first = wave * per, end = min(first + per, kb);
+    // block b: zeros past K and past this wavefront's range
+    auto load = [&](Stage& s, int b) {
+        const uint32_t k = (uint32_t)b * 128;
+        const uint32_t d = b < end ? 0u : kOOB;
+        const uint32_t d0 = d | ((int)k + 16 * g < K ? 0u : kOOB), d1 = d | ((int)k + 16 * g + 64 < K ? 0u : kOOB);
 #pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int64_t col = n0 + 8 * (v / 4) + 4 * hk + v % 4;
-                if (col < p.N) store_y(p, out, col, t[v]);
+        for (int j = 0; j < NT; j++) s.w[j] = load32(rW, offW, k + 16 * j * (uint32_t)p.ldw, d0, d1);
+        s.sw = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rV, d, b * 4, 0));
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            s.a[i] = load32(rA, offA[i], k, d0, d1);
+            s.sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rS, offS[i] | d, b * 4, 0));
+        }
+    };
+    f32x4 t[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) t[i][j] = f32x4{};
+#pragma unroll
+    for (int d = 0; d < D; d++) load(st[d], first + d);
+    for (int b = first; b < end; b += D) {
+#pragma unroll
+        for (int d = 0; d < D; d++) {
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                const float s = st[d].sa[i] * st[d].sw;
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    const f32x4 c = mfma128<FW, FA>(st[d].w[j], st[d].a[i], f32x4{});
+#pragma unroll
+                    for (int v = 0; v < 4; v++) t[i][j][v] = __builtin_fmaf(c[v], s, t[i][j][v]);
+                }
             }
+            load(st[d], b + d + D);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) part[wave][i * NT + j][lane] = t[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+            if ((i * NT + j) % KS != wave) continue;
+            f32x4 v = part[0][i * NT + j][lane];
+#pragma unroll
+            for (int q = 1; q < KS; q++) v += part[q][i * NT + j][lane];
+            if (out[i] >= 0) store_y4(p, out[i], n0 + 16 * j + 4 * g, v[0], v[1], v[2], v[3]);
         }
     }
 }
 
-template <int FW, int FA>
-static hipError_t launch_direct(const BlockGemmParams& p, hipStream_t s) {
-    const int64_t tiles = (p.M + 63) / 64;
-    const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)(tiles > 1024 ? 1024 : tiles), (unsigned)(p.experts ? p.experts : 1));
-    block_gemm_direct_kernel<FW, FA><<<grid, 256, 0, s>>>(p);
+template <int FW, int FA, int MT, int NT, int KS, int D>
+static hipError_t launch_stream(const BlockGemmParams& p, hipStream_t s) {
+    const int64_t grid_n = (p.N + 16 * NT - 1) / (16 * NT);
+    if (p.experts) {
+        const int64_t most = p.M / (16 * MT) + (p.experts < p.M ? p.experts : p.M);
+        block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, true><<<(unsigned)(most * grid_n), 64 * KS, 0, s>>>(p, 0, (int)grid_n);
+    } else {
+        const int64_t grid_m = (p.M + 16 * MT - 1) / (16 * MT);
+        block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, false>
+            <<<(unsigned)(grid_m * grid_n), 64 * KS, 0, s>>>(p, (int)grid_m, (int)grid_n);
+    }
     return hipGetLastError();
 }
 
-template <int FW, int FA, int BM, int BN, int WM, int WN>
+template <int FW, int FA, int BM, int BN, int WM, int WN, int S>
 static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
     const int64_t grid_n = (p.N + BN - 1) / BN;
     if (p.experts) {
         const int64_t most = p.M / BM + (p.experts < p.M ? p.experts : p.M);  // m-tiles, however the slots fall
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, true><<<(unsigned)(most * grid_n), 64 * WM * WN, 0, s>>>(p, 0, (int)grid_n);
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, true><<<(unsigned)(most * grid_n), 64 * WM * WN, 0, s>>>(p, 0, (int)grid_n);
     } else {
         const int64_t grid_m = (p.M + BM - 1) / BM;
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, false>
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, false>
             <<<(unsigned)(grid_m * grid_n), 64 * WM * WN, 0, s>>>(p, (int)grid_m, (int)grid_n);
     }
     return hipGetLastError();
 }
 
+// Which kernel.  Few rows: the streaming kernel, wide enough in N that A is read little and
+// narrow enough that half the compute units have a workgroup (5120 x 5120, one row: 16 / 32 /
+// 64 columns 11.5 / 8.3 / 13.5 us; 11008 x 4096: 12.5 / 12.0 / 11.4; 4096 x 13824, four rows:
+// 14.4 / 18.7 / 31.6).  From 65 rows on, tiles: a step of 128 of K takes about 2.0 us with a
+// 256 x 256 tile on every compute unit, 1.15 with two 128 x 128 ones (0.85 with one), 0.5 with
+// two 64 x 64 ones; the fewest rounds of steps win (us, 256 / 128 / 64: 203 x 4100 x 2080 33 /
+// 17 / 12; 1024 x 4096 x 4096 61 / 31 / 37; 2048 x 4096 x 4096 65 / 43 / 71; 4096 x 15360 x
+// 5120 338 / 369 / 612).
 template <int FW, int FA>
 static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
-    const int64_t rows = p.experts ? p.M / p.experts : p.M;
-    if (rows >= 256) return launch_tiles<FW, FA, 256, 256, 2, 4>(p, s);
-    return launch_direct<FW, FA>(p, s);
+    // experts: lists of the mean length, each with half a tile to spare
+    const double lists = p.experts ? (double)(p.experts < p.M ? p.experts : p.M) : 1.0, rows = (double)p.M / lists;
+    if (rows <= 16) {
+        const double wgs = lists * (double)p.N;
+        if (wgs >= 64 * 150) return launch_stream<FW, FA, 1, 4, 4, 4>(p, s);
+        if (wgs >= 32 * 150) return launch_stream<FW, FA, 1, 2, 4, 4>(p, s);
+        return launch_stream<FW, FA, 1, 1, 8, 4>(p, s);
+    }
+    if (rows <= 64) return launch_stream<FW, FA, 2, 2, 4, 3>(p, s);
+    auto tiles = [&](int b) {
+        const double m = p.experts ? lists * (rows / b + 0.5) : (double)((p.M + b - 1) / b);
+        return m * (double)((p.N + b - 1) / b);
+    };
+    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t64 = 0.5 * std::ceil(tiles(64) / 512);
+    const double t128 = tiles(128) <= 256 ? 0.85 : 1.15 * std::ceil(tiles(128) / 512);
+    if (t256 <= t128 && t256 <= t64) return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
+    if (t128 <= t64) return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
+    return launch_tiles<FW, FA, 64, 64, 2, 2, 4>(p, s);
 }
 
 hipError_t launch_gemm_block(const BlockGemmParams& in, hipStream_t s) {
