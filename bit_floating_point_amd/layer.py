@@ -97,28 +97,41 @@ def _need(ok, message):
         raise ValueError(message)
 
 
+# The checks below run on every call, beside kernels of a few microseconds: one condition
+# each, the message made only when it fails.
 def _matrix(t, name, rows, cols, dev, dtype=None):
     """Leading dimension of the row-major [rows, cols] tensor t."""
-    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols, f"{name} must be [{rows}, {cols}]")
-    _need(t.device == dev, f"{name} must be on {dev}")
-    if dtype is not None:
-        _need(t.dtype == dtype, f"{name} must be {dtype}")
+    if t.shape != (rows, cols) or t.device != dev or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be [{rows}, {cols}]{f' {dtype}' if dtype else ''} on {dev}, "
+                         f"not {list(t.shape)} {t.dtype} on {t.device}")
     ld, step = t.stride()
-    _need(step == 1 or cols <= 1, f"{name} must be row-major")
-    return ld if rows > 1 else max(ld, cols)
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be row-major")
+    return ld if rows > 1 or ld > cols else cols
 
 
 def _flat(t, name, count, dtype, dev):
     """Pointer of a contiguous tensor of `count` values (None: 0)."""
     if t is None:
         return None
-    _need(t.dtype == dtype and t.device == dev and t.is_contiguous() and t.numel() == count,
-          f"{name} must be a contiguous {dtype} tensor of {count} values on {dev}")
+    if t.numel() != count or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} values on {dev}")
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
+    """The current HIP stream of a device."""
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _check(status, func):
+    if status:
+        L.check(status, func)
 
 
 def _units(g, rows, cols):
@@ -172,7 +185,7 @@ def fp4_rmsnorm_quant(x: torch.Tensor, gamma: torch.Tensor, grid: L.fp4_grid | N
         _flat(gamma, "gamma", cols, gamma.dtype, dev), eps, _type(y, "y") if y is not None else 0,
         y.data_ptr() if y is not None else None, _matrix(y, "y", rows, cols, dev) if y is not None else 0,
         grid if grid is not None else _NO_GRID, g if g is not None else L.fp4_gran(), *tail)
-    L.check(_call("fp4_rmsnorm_quant")(d, _stream(dev)), "fp4_rmsnorm_quant")
+    _check(_call("fp4_rmsnorm_quant")(d, _stream(dev)), "fp4_rmsnorm_quant")
     return packed, scales
 
 
@@ -185,7 +198,7 @@ def fp4_swiglu_quant(x: torch.Tensor, grid: L.fp4_grid, g: L.fp4_gran, tensor_sc
     rows, cols, dev = x.shape[0], x.shape[1] // 2, x.device
     packed, scales, tail = _code_output(g, rows, cols, dev, tensor_scale, col_shift, packed, scales)
     d = fp4_swiglu8_desc(rows, cols, x.data_ptr(), _matrix(x, "x", rows, 2 * cols, dev), _type(x, "x"), 0, grid, g, *tail)
-    L.check(_call("fp4_swiglu_quant")(d, _stream(dev)), "fp4_swiglu_quant")
+    _check(_call("fp4_swiglu_quant")(d, _stream(dev)), "fp4_swiglu_quant")
     return packed, scales
 
 
@@ -204,7 +217,7 @@ def fp4_quantize_block(w: torch.Tensor, grid: L.fp4_grid, packed: torch.Tensor |
     _need((w.stride(-1) == 1 and packed.stride(-1) == 1) or k <= 1, "w and packed must be row-major")
     batch = lead[0] if lead else 1
     _flat(scales, "scales", batch * blocks[0] * blocks[1], torch.float32, dev)
-    L.check(_call("fp4_quantize_block")(
+    _check(_call("fp4_quantize_block")(
         w.data_ptr(), _type(w, "w"), batch, n, k, max(w.stride(-2), k), w.stride(0) if lead else 0, grid, packed.data_ptr(),
         max(packed.stride(-2), k), packed.stride(0) if lead else 0, scales.data_ptr(), _stream(dev)), "fp4_quantize_block")
     return packed, scales
@@ -231,7 +244,7 @@ def fp4_gemm_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_s
         a_grid, w.data_ptr(), _matrix(w, "w", N, K, dev, torch.uint8), w_scales.data_ptr(),
         _matrix(w_scales, "w_scales", -(-N // BLOCK), -(-K // BLOCK), dev, torch.float32), w_grid, y.data_ptr(),
         _matrix(y, "y", M, N, dev), _type(y, "y"), 0)
-    L.check(_call("fp4_gemm_block")(d, _stream(dev)), "fp4_gemm_block")
+    _check(_call("fp4_gemm_block")(d, _stream(dev)), "fp4_gemm_block")
     return y
 
 
@@ -266,7 +279,7 @@ def fp4_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
         _flat(bias, "bias", E, torch.float32, dev), groups, top_groups, group_top, int(bool(renormalise)), scale, 0,
         _flat(experts, "experts", T * top_k, torch.int32, dev), _flat(weights, "weights", T * top_k, torch.float32, dev),
         _flat(offsets, "offsets", E + 1, torch.int32, dev), _flat(slots, "slots", T * top_k, torch.int32, dev))
-    L.check(_call("fp4_route")(d, workspace.data_ptr() if need else None, need, _stream(dev)), "fp4_route")
+    _check(_call("fp4_route")(d, workspace.data_ptr() if need else None, need, _stream(dev)), "fp4_route")
     return Routing(experts, weights, offsets, slots)
 
 
@@ -289,5 +302,5 @@ def fp4_gemm_experts(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
         _flat(w_scales, "w_scales", E * -(-N // BLOCK) * -(-K // BLOCK), torch.float32, dev), w_grid,
         _flat(offsets, "offsets", E + 1, torch.int32, dev), _flat(slots, "slots", S, torch.int32, dev), y.data_ptr(),
         _matrix(y, "y", S, N, dev), _type(y, "y"), 0)
-    L.check(_call("fp4_gemm_experts")(d, _stream(dev)), "fp4_gemm_experts")
+    _check(_call("fp4_gemm_experts")(d, _stream(dev)), "fp4_gemm_experts")
     return y
