@@ -291,14 +291,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
     };
 #pragma unroll
     for (int c = 0; c < 8; c++) load_scales(0, c);
-#pragma unroll
-    for (int q = 0; q < S - 1; q++) load_scales(1, q);
+    // (every stage but the first brings GROUP loads, as in the loop: the waits count them)
 #pragma unroll
     for (int q = 0; q < S; q++) {
         load_w(q, q * STAGE);
+        if (q > 0) load_scales(1, q - 1);
         load_a(q, q * STAGE);
     }
-    step_barrier<(S - 1) * (LA + LB)>();
+    step_barrier<(S - 1) * GROUP>();
     uint32_t cur = 0;
     for (int b = 0; b < kb; b++) {
         const uint8_t* sa = smem + cur;

@@ -18,33 +18,70 @@ namespace fp4 {
 
 namespace {
 
-constexpr float kNone = -INFINITY;  // key of an expert that cannot be chosen
+constexpr int kNone = INT32_MIN;    // key of an expert that cannot be chosen
 constexpr int kMaxE = 1024;
 constexpr int kRanges = 256;        // ranges of tokens counted apart, at most
 constexpr int kSmallSlots = 1024, kSmallTokens = 64;  // one workgroup routes and places these
 constexpr float kLog2e = 0x1.715476p+0f;
 
-// v of the lane that a DPP control names (lanes without a source keep v)
+// Keys are compared as integers in the order of their floats (-0 as 0): one instruction per
+// step of a maximum.  Its inverse gives the float back.
+__device__ __forceinline__ int ordered(float v) {
+    const int b = __float_as_int(v + 0.0f);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// v of the lane that a DPP control names
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false));
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ int dpp_max(int v) {  // lanes without a source keep v
+    return max(v, __builtin_amdgcn_update_dpp(kNone, v, CTRL, 0xF, 0xF, false));
 }
 
 // largest v of the wavefront, uniform
-__device__ __forceinline__ float max64(float v) {
-    v = fmaxf(v, dpp<0xB1>(v));   // neighbours
-    v = fmaxf(v, dpp<0x4E>(v));   // pairs
-    v = fmaxf(v, dpp<0x141>(v));  // halves of 8
-    v = fmaxf(v, dpp<0x140>(v));  // halves of 16
-    v = fmaxf(v, dpp<0x142>(v));  // row 0 into 1, 2 into 3
-    v = fmaxf(v, dpp<0x143>(v));  // rows 0, 1 into 2, 3
+__device__ __forceinline__ int max64(int v) {
+    v = dpp_max<0xB1>(v);   // neighbours
+    v = dpp_max<0x4E>(v);   // pairs
+    v = dpp_max<0x141>(v);  // halves of 8
+    v = dpp_max<0x140>(v);  // halves of 16
+    v = dpp_max<0x142>(v);  // row 0 into 1, 2 into 3
+    v = dpp_max<0x143>(v);  // rows 0, 1 into 2, 3
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
+// sum of v over the wavefront, uniform
+__device__ __forceinline__ float sum64(float v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-__device__ __forceinline__ float sum64(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+// sum of v over this lane and those below
+__device__ __forceinline__ int scan64(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row shifts by 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
     return v;
+}
+
+// the two largest of this lane's (a, b) and those of the lane that a DPP control names
+template <int CTRL>
+__device__ __forceinline__ void merge2(int& a, int& b) {
+    const int c = __builtin_amdgcn_update_dpp(0, a, CTRL, 0xF, 0xF, false);
+    const int d = __builtin_amdgcn_update_dpp(0, b, CTRL, 0xF, 0xF, false);
+    b = max(min(a, c), max(b, d));
+    a = max(a, c);
 }
 
 // score of a usable logit; softmax: top is the largest logit, rsum one over the sum
@@ -59,74 +96,115 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e
                          : reinterpret_cast<const float*>(p.logits)[at];
 }
 
+// A lane's part of a wavefront's work: its experts base .. base + count - 1 and their biases.
+template <int EPL>
+struct Lane {
+    int lane, group, place, base, count;
+    float bias[EPL];
+
+    __device__ __forceinline__ Lane(const RouteParams& p, int lg_bits) {
+        lane = threadIdx.x & 63;
+        const int size = p.experts / p.groups;
+        group = lane >> lg_bits;
+        place = (lane & ((1 << lg_bits) - 1)) * EPL;  // within the group
+        base = group * size + place;
+        count = group < p.groups ? max(min(size - place, EPL), 0) : 0;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) bias[i] = p.bias && i < count ? p.bias[base + i] : 0.0f;
+    }
+};
+
+// this lane's logits of token t (`whole`: its run is one aligned load)
+template <int EPL>
+__device__ __forceinline__ void load_logits(const RouteParams& p, const Lane<EPL>& me, int64_t t, bool whole, float (&v)[EPL]) {
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) v[i] = INFINITY;
+        if (me.count == EPL) {
+            const int64_t at = t * p.ld + me.base;
+            constexpr int W = EPL < 4 ? EPL : 4;  // values per load
+            if (p.logits_bf16) {
+                struct alignas(2 * W) Part { uint16_t v[W]; };
+                const Part* q = reinterpret_cast<const Part*>(reinterpret_cast<const uint16_t*>(p.logits) + at);
+#pragma unroll
+                for (int i = 0; i < EPL; i++) v[i] = bf16_bits_to_float(q[i / W].v[i % W]);
+            } else {
+                struct alignas(4 * W) Part { float v[W]; };
+                const Part* q = reinterpret_cast<const Part*>(reinterpret_cast<const float*>(p.logits) + at);
+#pragma unroll
+                for (int i = 0; i < EPL; i++) v[i] = q[i / W].v[i % W];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) v[i] = i < me.count ? logit_at(p, t, me.base + i) : INFINITY;
+    }
+}
+
 // The choice for token t, written out; lane j < top_k returns the j-th expert (or -1).
 template <int EPL>
-__device__ __forceinline__ int choose(const RouteParams& p, int64_t t, int lane, int lg_bits, const float* bias) {
-    const int group = lane >> lg_bits, size = p.experts / p.groups;
-    const int place = (lane & ((1 << lg_bits) - 1)) * EPL;  // within the group
-    const int base = group * size + place, count = group < p.groups ? min(size - place, EPL) : 0;
-    float key[EPL];
-    int idx[EPL];
-    float top = kNone;
+__device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const Lane<EPL>& me, const float (&logit)[EPL], int lg_bits) {
+    const int lane = me.lane, group = me.group;
+    int key[EPL], idx[EPL];
+    int best = kNone;
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
-        float v = kNone;
-        if (i < count) {
-            v = logit_at(p, t, base + i);
-            if (!(fabsf(v) < INFINITY)) v = kNone;  // infinite or NaN: not usable
-        }
-        key[i] = v;
-        idx[i] = base + i;
-        top = fmaxf(top, v);
+        // infinite or NaN: not usable
+        key[i] = fabsf(logit[i]) < INFINITY ? ordered(logit[i]) : kNone;
+        idx[i] = me.base + i;
+        best = max(best, key[i]);
     }
-    float rsum = 0.0f;
+    float top = 0.0f, rsum = 0.0f;
     if (!p.sigmoid) {
-        top = max64(top);
+        top = unordered(max64(best));
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) s += key[i] == kNone ? 0.0f : __builtin_amdgcn_exp2f(kLog2e * (key[i] - top));
+        for (int i = 0; i < EPL; i++) s += key[i] == kNone ? 0.0f : __builtin_amdgcn_exp2f(kLog2e * (unordered(key[i]) - top));
         rsum = 1.0f / sum64(s);
     }
     // Keys: score + bias; without a bias the logit, which has the scores' order and neither
     // rounds nor underflows.
-    if (bias) {
+    if (p.bias) {
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            if (key[i] != kNone) key[i] = score_of(key[i], p.sigmoid, top, rsum) + bias[base + i];
+            key[i] = key[i] == kNone ? kNone : ordered(score_of(logit[i], p.sigmoid, top, rsum) + me.bias[i]);
     }
 #pragma unroll
     for (int a = 0; a + 1 < EPL; a++) {  // largest first; equal keys stay in order
 #pragma unroll
         for (int b = EPL - 1; b > a; b--) {
             const bool swap = key[b] > key[b - 1];
-            const float k = key[b];
-            const int x = idx[b];
-            key[b] = swap ? key[b - 1] : k;
+            const int k = key[b], x = idx[b];
+            key[b] = min(k, key[b - 1]);
+            key[b - 1] = max(k, key[b - 1]);
             idx[b] = swap ? idx[b - 1] : x;
-            key[b - 1] = swap ? k : key[b - 1];
             idx[b - 1] = swap ? x : idx[b - 1];
         }
     }
     if (p.groups > 1) {
         // the group's two best values, in all of its lanes
-        float a = key[0], b = EPL > 1 ? key[EPL > 1 ? 1 : 0] : kNone;
-        if (!bias) {
-            a = a == kNone ? a : score_of(a, p.sigmoid, top, rsum);
-            b = b == kNone ? b : score_of(b, p.sigmoid, top, rsum);
+        int a = key[0], b = EPL > 1 ? key[EPL > 1 ? 1 : 0] : kNone;
+        if (!p.bias) {
+            if (a != kNone) a = ordered(score_of(unordered(a), p.sigmoid, top, rsum));
+            if (b != kNone) b = ordered(score_of(unordered(b), p.sigmoid, top, rsum));
         }
-        for (int o = 1; o < (1 << lg_bits); o <<= 1) {
-            const float c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
-            b = fmaxf(fminf(a, c), fmaxf(b, d));
-            a = fmaxf(a, c);
+        // steps of 1, 2, 4 and 8 lanes (a mirrored half of equal values serves as the step)
+        if (lg_bits > 0) merge2<0xB1>(a, b);
+        if (lg_bits > 1) merge2<0x4E>(a, b);
+        if (lg_bits > 2) merge2<0x141>(a, b);
+        if (lg_bits > 3) merge2<0x140>(a, b);
+        if (lg_bits > 4) {  // two groups: a 32-lane half each
+            const int c = __shfl_xor(a, 16, 64), d = __shfl_xor(b, 16, 64);
+            b = max(min(a, c), max(b, d));
+            a = max(a, c);
         }
-        float value = p.group_top == 2 && b != kNone ? a + b : a;
-        if (place != 0 || group >= p.groups) value = kNone;
+        int value = p.group_top == 2 && b != kNone ? ordered(unordered(a) + unordered(b)) : a;
+        if (me.place != 0 || group >= p.groups) value = kNone;
         uint64_t kept = 0;
         for (int j = 0; j < p.top_groups; j++) {
-            const float m = max64(value);
-            const uint64_t at = __ballot(value == m && m != kNone);
-            if (!at) break;
-            const int l = __ffsll((unsigned long long)at) - 1;
+            const int m = max64(value);
+            if (m == kNone) break;
+            const int l = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(value == m)) - 1;
             kept |= 1ull << (l >> lg_bits);
             if (lane == l) value = kNone;
         }
@@ -137,20 +215,19 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, int lane,
     }
     int mine = -1;
     for (int j = 0; j < p.top_k; j++) {
-        const float m = max64(key[0]);
-        const uint64_t at = __ballot(key[0] == m && m != kNone);
-        if (!at) break;
-        const int l = __ffsll((unsigned long long)at) - 1;
+        const int m = max64(key[0]);
+        if (m == kNone) break;
+        const int l = __ffsll((unsigned long long)__builtin_amdgcn_ballot_w64(key[0] == m)) - 1;
         const int e = __builtin_amdgcn_readlane(idx[0], l);
-        if (lane == j) mine = e;
-        if (lane == l) {
+        mine = lane == j ? e : mine;
+        // its lane moves on (bitwise selects: one instruction each)
+        const int taken = lane == l ? -1 : 0;
 #pragma unroll
-            for (int i = 0; i + 1 < EPL; i++) {
-                key[i] = key[i + 1];
-                idx[i] = idx[i + 1];
-            }
-            key[EPL - 1] = kNone;
+        for (int i = 0; i + 1 < EPL; i++) {
+            key[i] = (key[i + 1] & taken) | (key[i] & ~taken);
+            idx[i] = (idx[i + 1] & taken) | (idx[i] & ~taken);
         }
+        key[EPL - 1] = (kNone & taken) | (key[EPL - 1] & ~taken);
     }
     float w = 0.0f;
     if (mine >= 0) w = score_of(logit_at(p, t, mine), p.sigmoid, top, rsum);
@@ -165,20 +242,17 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, int lane,
     return mine;
 }
 
-// exclusive sums of n values of LDS, by one wavefront; dst may be src
-__device__ __forceinline__ void exclusive(const int* src, int* dst, int n, int lane) {
+// total[0 .. n) -> its exclusive sums, by 16 wavefronts (n <= 1025; `chunk`: LDS)
+__device__ __forceinline__ void exclusive(int* total, int* chunk, int n) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int c = tid < n ? total[tid] : 0, s = scan64(c);
+    if (lane == 63) chunk[wave] = s;
+    __syncthreads();
     int carry = 0;
-    for (int e0 = 0; e0 < n; e0 += 64) {
-        const int c = e0 + lane < n ? src[e0 + lane] : 0;
-        int s = c;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(s, o, 64);
-            if (lane >= o) s += u;
-        }
-        if (e0 + lane < n) dst[e0 + lane] = carry + s - c;
-        carry += __shfl(s, 63, 64);
-    }
+    for (int w = 0; w < wave; w++) carry += chunk[w];
+    if (tid < n) total[tid] = carry + s - c;
+    if (tid == 1023 && n == 1025) total[1024] = carry + s;
+    __syncthreads();
 }
 
 // Places slots [first, last) of the list behind at[e] of each expert's part (at: this
@@ -208,47 +282,40 @@ __device__ __forceinline__ void place(const RouteParams& p, int64_t first, int64
 
 }  // namespace
 
-// Choice for the tokens of one range per workgroup (8 wavefronts), and the range's counts.
+// Choice for the tokens of one range per workgroup (16 wavefronts), and the range's counts:
+// a row of `stride` values, zeros past the experts.
 template <int EPL>
-__global__ void __launch_bounds__(512) route_kernel(RouteParams p, int per_range, int lg_bits) {
-    __shared__ int hist[kMaxE + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = p.experts;
-    for (int e = threadIdx.x; e <= E; e += 512) hist[e] = 0;
+__global__ void __launch_bounds__(1024) route_kernel(RouteParams p, int per_range, int lg_bits, int stride, bool whole) {
+    __shared__ int hist[kMaxE];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Lane<EPL> me(p, lg_bits);
+    if (threadIdx.x < stride) hist[threadIdx.x] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * per_range, last = min(first + per_range, p.tokens);
-    for (int64_t t = first + wave; t < last; t += 8) {
-        const int e = choose<EPL>(p, t, lane, lg_bits, p.bias);
-        if (p.offsets && lane < p.top_k) atomicAdd(&hist[e < 0 ? E : e], 1);  // a count: any order
+    float next[EPL];
+    if (first + wave < last) load_logits<EPL>(p, me, first + wave, whole, next);
+    for (int64_t t = first + wave; t < last; t += 16) {
+        float logit[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; i++) logit[i] = next[i];
+        if (t + 16 < last) load_logits<EPL>(p, me, t + 16, whole, next);
+        const int e = choose<EPL>(p, t, me, logit, lg_bits);
+        if (e >= 0) atomicAdd(&hist[e], 1);  // a count: any order
     }
     if (!p.offsets) return;
     __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += 512) p.counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+    if (threadIdx.x < stride) p.counts[(int64_t)blockIdx.x * stride + threadIdx.x] = hist[threadIdx.x];
 }
 
 // Slots of `ranges` consecutive ranges per workgroup (16 wavefronts).
-__global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nranges, int ranges, int64_t range_slots) {
-    __shared__ int before[kMaxE + 1], total[kMaxE + 1], part[16][kMaxE + 1];
+__global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nranges, int ranges, int64_t range_slots, int stride) {
+    __shared__ int before[kMaxE + 1], total[kMaxE + 1], chunk[16];
+    __shared__ int part[16][kMaxE + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.experts;
-    for (int e = tid; e <= E; e += 1024) {
-        before[e] = total[e] = 0;
-        for (int w = 0; w < 16; w++) part[w][e] = 0;
-    }
+    for (int e = tid; e <= E; e += 1024) before[e] = total[e] = 0;
+    for (int e = lane; e <= E; e += 64) part[wave][e] = 0;
     __syncthreads();
     const int r0 = blockIdx.x * ranges;
-    for (int e0 = 0; e0 <= E; e0 += 64) {
-        const int e = e0 + lane;
-        int b = 0, all = 0;
-        if (e <= E) {
-#pragma unroll 8
-            for (int r = wave; r < nranges; r += 16) {
-                const int c = p.counts[(int64_t)r * (E + 1) + e];
-                all += c;
-                b += r < r0 ? c : 0;
-            }
-            atomicAdd(&total[e], all);
-            atomicAdd(&before[e], b);
-        }
-    }
     const int64_t nslots = p.tokens * p.top_k, first = r0 * range_slots, last = min(first + ranges * range_slots, nslots);
     const int64_t quota = (last - first + 1023) / 1024 * 64;  // slots per wavefront
     const int64_t w0 = min(first + wave * quota, last), w1 = min(w0 + quota, last);
@@ -257,12 +324,35 @@ __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nr
         return e < 0 ? E : e;
     };
     for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&part[wave][expert(s)], 1);
+    int sum = 0;
+    for (int e = lane * 4; e < stride; e += 256) {
+        int4 all = make_int4(0, 0, 0, 0), b = all;
+#pragma unroll 16
+        for (int r = wave; r < nranges; r += 16) {
+            const int4 c = *reinterpret_cast<const int4*>(p.counts + (int64_t)r * stride + e);
+            const int in = r < r0 ? -1 : 0;
+            all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+            b.x += c.x & in, b.y += c.y & in, b.z += c.z & in, b.w += c.w & in;
+        }
+        const int va[4] = {all.x, all.y, all.z, all.w}, vb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (e + i < E) {
+                atomicAdd(&total[e + i], va[i]);
+                atomicAdd(&before[e + i], vb[i]);
+                sum += vb[i];
+            }
+        }
+    }
+    sum = scan64(sum);
+    if (lane == 63) atomicSub(&before[E], sum);
     __syncthreads();
-    if (wave == 0) exclusive(total, total, E + 1, lane);
-    __syncthreads();
+    exclusive(total, chunk, E + 1);
     for (int e = tid; e <= E; e += 1024) {
         if (blockIdx.x == 0) p.offsets[e] = total[e];
-        int at = total[e] + before[e];
+        // slots without an expert: those before the range that no expert has
+        int at = total[e] + before[e] + (e == E ? (int)first : 0);
+#pragma unroll
         for (int w = 0; w < 16; w++) {
             const int c = part[w][e];
             part[w][e] = at;
@@ -275,19 +365,19 @@ __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nr
 
 // Few tokens: choice and layout in one workgroup (16 wavefronts).
 template <int EPL>
-__global__ void __launch_bounds__(1024) route_small_kernel(RouteParams p, int lg_bits) {
-    __shared__ int part[16][kMaxE + 1], total[kMaxE + 1];
+__global__ void __launch_bounds__(1024) route_small_kernel(RouteParams p, int lg_bits, bool whole) {
+    __shared__ int part[16][kMaxE + 1], total[kMaxE + 1], chunk[16];
     __shared__ int chosen[kSmallSlots];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.experts;
-    if (p.offsets) {
-        for (int e = tid; e <= E; e += 1024)
-            for (int w = 0; w < 16; w++) part[w][e] = 0;
-        __syncthreads();
-    }
+    if (p.offsets)  // a wavefront's own counts
+        for (int e = lane; e <= E; e += 64) part[wave][e] = 0;
     // a wavefront takes consecutive tokens, so its slots are consecutive too
+    const Lane<EPL> me(p, lg_bits);
     const int T = (int)p.tokens, per = (T + 15) / 16, t0 = min(wave * per, T), t1 = min(t0 + per, T);
     for (int t = t0; t < t1; t++) {
-        const int e = choose<EPL>(p, t, lane, lg_bits, p.bias);
+        float logit[EPL];
+        load_logits<EPL>(p, me, t, whole, logit);
+        const int e = choose<EPL>(p, t, me, logit, lg_bits);
         if (p.offsets && lane < p.top_k) {
             chosen[t * p.top_k + lane] = e < 0 ? E : e;
             atomicAdd(&part[wave][e < 0 ? E : e], 1);
@@ -297,15 +387,16 @@ __global__ void __launch_bounds__(1024) route_small_kernel(RouteParams p, int lg
     __syncthreads();
     for (int e = tid; e <= E; e += 1024) {
         int n = 0;
+#pragma unroll
         for (int w = 0; w < 16; w++) n += part[w][e];
         total[e] = n;
     }
     __syncthreads();
-    if (wave == 0) exclusive(total, total, E + 1, lane);
-    __syncthreads();
+    exclusive(total, chunk, E + 1);
     for (int e = tid; e <= E; e += 1024) {
         int at = total[e];
         p.offsets[e] = at;
+#pragma unroll
         for (int w = 0; w < 16; w++) {
             const int c = part[w][e];
             part[w][e] = at;
@@ -330,27 +421,34 @@ static int64_t route_range(int64_t tokens) {
     return r < 16 ? 16 : r;
 }
 
+static int route_stride(int experts) { return (experts + 3) & ~3; }
+
 size_t route_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k) {
     if (route_small(tokens, top_k)) return 0;
     const int64_t per = route_range(tokens);
-    return (size_t)((tokens + per - 1) / per) * (size_t)(experts + 1) * sizeof(int32_t);
+    return (size_t)((tokens + per - 1) / per) * (size_t)route_stride(experts) * sizeof(int32_t);
 }
 
 template <int EPL>
 static hipError_t launch_choice(const RouteParams& p, int lg_bits, hipStream_t s) {
+    // whether every lane's run of experts is whole and aligned for one load (of 16 bytes at most)
+    const int size = p.experts / p.groups, bytes = (p.logits_bf16 ? 2 : 4) * (EPL < 4 ? EPL : 4);
+    const bool whole = EPL > 1 && size % EPL == 0 && p.ld % EPL == 0 && reinterpret_cast<uintptr_t>(p.logits) % bytes == 0;
+
     if (route_small(p.tokens, p.top_k)) {
         const int waves = p.offsets || p.tokens >= 16 ? 16 : (int)p.tokens;
-        route_small_kernel<EPL><<<1, 64 * (p.offsets ? 16 : waves), 0, s>>>(p, lg_bits);
+        route_small_kernel<EPL><<<1, 64 * (p.offsets ? 16 : waves), 0, s>>>(p, lg_bits, whole);
         return hipGetLastError();
     }
     const int64_t per = route_range(p.tokens), nranges = (p.tokens + per - 1) / per;
-    route_kernel<EPL><<<(unsigned)nranges, 512, 0, s>>>(p, (int)per, lg_bits);
+    route_kernel<EPL><<<(unsigned)nranges, 1024, 0, s>>>(p, (int)per, lg_bits, route_stride(p.experts), whole);
     if (p.offsets) {
         const int64_t nslots = p.tokens * p.top_k;
         int64_t wgs = (nslots + 2047) / 2048;
         if (wgs > 64) wgs = 64;
         const int64_t ranges = (nranges + wgs - 1) / wgs;
-        route_place_kernel<<<(unsigned)((nranges + ranges - 1) / ranges), 1024, 0, s>>>(p, (int)nranges, (int)ranges, per * p.top_k);
+        route_place_kernel<<<(unsigned)((nranges + ranges - 1) / ranges), 1024, 0, s>>>(p, (int)nranges, (int)ranges, per * p.top_k,
+                                                                                           route_stride(p.experts));
     }
     return hipGetLastError();
 }
