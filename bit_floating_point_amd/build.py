@@ -26,9 +26,9 @@ CFLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-ffp-contract
           "-Wno-unused-command-line-argument"]
 
 
-# The persistent GEMM kernels count their outstanding loads in their waits; a register
-# spill would add scratch memory operations to those counts, so they must not spill.
-NO_SPILL = ("gemm_w4a4.hip", "gemm_lut.hip")
+# These GEMM kernels count their outstanding loads in their waits; a register spill would
+# add scratch memory operations to those counts, so they must not spill.
+NO_SPILL = ("gemm_w4a4.hip", "gemm_lut.hip", "gemm_block.hip")
 
 
 def _check_no_spill(src: str, remarks: str) -> None:

@@ -63,6 +63,7 @@ fp4_status code_output(int64_t cols, const fp4_grid& grid, const fp4_gran& gran,
     out->group = gran.mode == FP4_SCALE_GROUP ? gran.group : 0;
     out->scale_f16 = gran.scale_dtype == FP4_F16;
     out->qmax = q.qmax;
+    out->rqmax = 1.0f / q.qmax;
     out->tensor_scale = tensor_scale;
     out->col_shift = col_shift;
     out->scales = scales;

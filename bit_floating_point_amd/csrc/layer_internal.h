@@ -27,7 +27,7 @@ struct CodeOut {
     int32_t mode;     // 0 tensor (scale given), 1 row, 2 group
     int32_t group;
     int32_t scale_f16;
-    float qmax;
+    float qmax, rqmax;  // largest magnitude and fl32 of one over it
     const float* tensor_scale;
     const int8_t* col_shift;
     void* scales;
