@@ -389,9 +389,10 @@ template <bool XBF>
 static hipError_t launch_norm(const NormParams& p, hipStream_t s) {
     const int64_t chunks = (p.cols + 7) / 8;
     const dim3 grid((unsigned)p.rows);
+    // (777 x 11016 f32 of one term: two chunks 28 us, four 32)
     const int few = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
     const int many = chunks <= 256 ? 1 : p.terms > 1 && chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
-    const int nc = p.rows < 512 ? few : many;
+    const int nc = p.rows < 1024 ? few : many;
     const int threads = 64 * waves_for(chunks, nc);
     if (nc == 1) rmsnorm_quant_kernel<1, XBF><<<grid, threads, 0, s>>>(p);
     else if (nc == 2) rmsnorm_quant_kernel<2, XBF><<<grid, threads, 0, s>>>(p);
