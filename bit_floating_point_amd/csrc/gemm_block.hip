@@ -153,21 +153,27 @@ __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n
 // S stages of 128 codes of K are in LDS or on their way there.
 // A workgroup of WM x WN wavefronts computes BM x BN outputs, each wavefront MT x NT
 // results of 32 x 32 (its m-tiles every WM-th of the tile's, so that a short tile's rows
-// spread over the wavefronts).
-template <int FW, int FA, int BM, int BN, int WM, int WN, int S, bool EXP>
-__global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockGemmParams p, int grid_m, int grid_n) {
+// spread over the wavefronts).  KG such groups of wavefronts share a tile: group g takes the
+// blocks g, KG + g, ... of K with stages of its own, and the sums are added in order at the
+// end -- for grids that leave a compute unit one workgroup, whose steps would follow each
+// other with nothing beside them.
+template <int FW, int FA, int BM, int BN, int WM, int WN, int S, int KG, bool EXP>
+__global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(BlockGemmParams p, int grid_m, int grid_n) {
     constexpr int NW = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
     constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
     // scales: chunks of 8 blocks of K, BM rows (and the column blocks of W) of 8 values
     constexpr int CH = BM * 32 + 256 * (NW - BM / 64), NCH = S > 2 ? 3 : 2;
     constexpr int LA = SA / 1024 / NW, LB = SB / 1024 / NW;
     static_assert(BM / 64 < NW, "one wavefront per 64 scales of A, one for those of W");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + NCH * CH];
+    constexpr int REGION = S * STAGE + (NCH * CH + 1023) / 1024 * 1024;  // of one group
+    __shared__ __attribute__((aligned(1024))) uint8_t smem_all[KG * REGION];
     __shared__ uint32_t scale_row[BM + 64];  // byte offset of the scales of each row, then of each column block
-    uint8_t* const smem_s = smem + S * STAGE;
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % NW);  // within its group
+    const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) / NW);
+    uint8_t* const smem = smem_all + kg * REGION;
+    uint8_t* const smem_s = smem + S * STAGE;
     const int wm = wave % WM, wn = wave / WM;
     const int r32 = lane & 31, hk = lane >> 5;
 
@@ -190,6 +196,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
     }
     const int64_t n0 = (int64_t)tile.n * BN;
     const int kb = (int)((p.K + 127) / 128), K = (int)p.K;
+    const int steps = (kb + KG - 1) / KG;  // step b of group g is block b KG + g
     // output row and source row of the tile's row r, or -1
     auto rows_of = [&](int r, int64_t& src) -> int64_t {
         const int64_t m = tile.m0 + r;
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
     }
     offB = (uint32_t)(r8 * (int)p.ldw + seg * 16);
     const uint32_t stepA = (uint32_t)(NW * 8 * (int)p.lda), stepB = (uint32_t)(NW * 8 * (int)p.ldw);
-    for (int r = threadIdx.x; r < BM + 64; r += 64 * NW) {
+    for (int r = threadIdx.x; r < BM + 64; r += 64 * NW * KG) {
         int64_t src = r - BM;
         if (r < BM) scale_row[r] = rows_of(r, src) < 0 ? kOOB : (uint32_t)(src * p.lda_s * 4);
         else scale_row[r] = src < nbs ? (uint32_t)(src * p.ldw_s * 4) : kOOB;
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
     const uint32_t lds_scale = __builtin_amdgcn_readfirstlane(lds + S * STAGE + wave * 256);
     // Pieces past K read zeros, and so do whole stages past it (the loop has no branch).
     auto load_a = [&](int b, uint32_t stage) {
-        const uint32_t k = (uint32_t)(b * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
+        const uint32_t k = (uint32_t)((b * KG + kg) * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
 #pragma unroll
         for (int i = 0; i < LA; i++) {
             if constexpr (EXP) lds_load16(rsA, offA[i] |= dead, k, lds_wave, stage + NW * i * 1024);
@@ -251,18 +258,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
         }
     };
     auto load_w = [&](int b, uint32_t stage) {
-        const uint32_t k = (uint32_t)(b * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
+        const uint32_t k = (uint32_t)((b * KG + kg) * 128), dead = (int)k + seg * 16 < K ? 0u : kOOB;
 #pragma unroll
         for (int i = 0; i < LB; i++) lds_load16(rsB, offB |= dead, k + i * stepB, lds_wave, stage + SA + NW * i * 1024);
     };
-    // Part c (of 8) of the scales' chunk q (blocks 8 q .. 8 q + 7): 8 values of BM / 8 rows,
+    // Part c (of 8) of the scales' chunk q (of steps 8 q .. 8 q + 7): 8 values of BM / 8 rows,
     // and with every part those of W.  A load instruction then touches 8 lines, not 64.
-    // Block k of row r sits at position k ^ (r / 8 % 8): the reads of 32 rows fall into
+    // Step k's of row r sits at position k ^ (r / 8 % 8): the reads of 32 rows fall into
     // different banks.
     auto load_scales = [&](int q, int c) {
         const int group = BM / 64 * c + wave;  // of 8 rows
         const uint32_t row = scale_row[(of_a ? 8 * group : BM + 8 * (wave - BM / 64)) + (lane >> 3)];
-        const int k = q * 8 + ((lane & 7) ^ (of_a ? group & 7 : 0));
+        const int k = (q * 8 + ((lane & 7) ^ (of_a ? group & 7 : 0))) * KG + kg;
         lds_load4(rsS, (row + (uint32_t)k * 4) | (k < kb ? 0u : kOOB), 0, lds_scale,
                   (uint32_t)(q % NCH) * CH + (of_a ? BM * 4 * c : BM * 28));
     };
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
     }
     step_barrier<(S - 1) * GROUP>();
     uint32_t cur = 0;
-    for (int b = 0; b < kb; b++) {
+    for (int b = 0; b < steps; b++) {
         const uint8_t* sa = smem + cur;
         const uint8_t* sb = sa + SA;
         const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) % NCH) * CH);
@@ -362,6 +369,37 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) block_gemm_tile_kernel(BlockG
         cur = cur + STAGE == S * STAGE ? 0 : cur + STAGE;
     }
     step_barrier<0>();  // no load into LDS outlives the workgroup
+
+    if constexpr (KG > 1) {
+        float4* part = reinterpret_cast<float4*>(smem_all);
+        auto at = [&](int g, int i, int j, int q) { return ((((g - 1) * NW + wave) * MT + i) * NT + j) * 4 + q; };
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        part[at(kg, i, j, q) * 64 + lane] =
+                            make_float4(t[i][j][4 * q], t[i][j][4 * q + 1], t[i][j][4 * q + 2], t[i][j][4 * q + 3]);
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int g = 1; g < KG; g++)
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const float4 v = part[at(g, i, j, q) * 64 + lane];
+                        t[i][j][4 * q] += v.x;
+                        t[i][j][4 * q + 1] += v.y;
+                        t[i][j][4 * q + 2] += v.z;
+                        t[i][j][4 * q + 3] += v.w;
+                    }
+    }
 
 #pragma unroll
     for (int i = 0; i < MT; i++) {
@@ -509,48 +547,54 @@ static hipError_t launch_stream(const BlockGemmParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int FW, int FA, int BM, int BN, int WM, int WN, int S>
+template <int FW, int FA, int BM, int BN, int WM, int WN, int S, int KG = 1>
 static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
     const int64_t grid_n = (p.N + BN - 1) / BN;
     if (p.experts) {
         const int64_t most = p.M / BM + (p.experts < p.M ? p.experts : p.M);  // m-tiles, however the slots fall
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, true><<<(unsigned)(most * grid_n), 64 * WM * WN, 0, s>>>(p, 0, (int)grid_n);
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, true><<<(unsigned)(most * grid_n), 64 * WM * WN * KG, 0, s>>>(p, 0, (int)grid_n);
     } else {
         const int64_t grid_m = (p.M + BM - 1) / BM;
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, false>
-            <<<(unsigned)(grid_m * grid_n), 64 * WM * WN, 0, s>>>(p, (int)grid_m, (int)grid_n);
+        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, false>
+            <<<(unsigned)(grid_m * grid_n), 64 * WM * WN * KG, 0, s>>>(p, (int)grid_m, (int)grid_n);
     }
     return hipGetLastError();
 }
 
-// Which kernel.  Few rows: the streaming kernel, wide enough in N that A is read little and
-// narrow enough that half the compute units have a workgroup (5120 x 5120, one row: 16 / 32 /
-// 64 columns 11.5 / 8.3 / 13.5 us; 11008 x 4096: 12.5 / 12.0 / 11.4; 4096 x 13824, four rows:
-// 14.4 / 18.7 / 31.6).  From 65 rows on, tiles: a step of 128 of K takes about 2.0 us with a
-// 256 x 256 tile on every compute unit, 1.15 with two 128 x 128 ones (0.85 with one), 0.5 with
-// two 64 x 64 ones; the fewest rounds of steps win (us, 256 / 128 / 64: 203 x 4100 x 2080 33 /
-// 17 / 12; 1024 x 4096 x 4096 61 / 31 / 37; 2048 x 4096 x 4096 65 / 43 / 71; 4096 x 15360 x
-// 5120 338 / 369 / 612).
+// Which kernel (us, measured one against the other).
+// Up to 16 rows the streaming kernel, as wide in N as leaves 150 workgroups: A is read once per
+// workgroup (16 / 32 / 64 columns: 5120 x 5120, one row 11.6 / 7.7 / 12.4; 11008 x 4096: 13.8 /
+// 11.3 / 11.1; 4096 x 13824, four rows 12.6 / 18.4 / 30.3).  At 17 rows and more the tiles win
+// (24 x 11008 x 4096: 15.0 against 15.9; 64 x 5120 x 5120 on the streaming kernel 14.6 against 13.3).
+// Tiles: a step of 128 of K takes about 2.0 us with a 256 x 256 tile on every compute unit, 1.2
+// with two 128 x 128 ones, 0.7 with one (two groups of wavefronts), 0.48 and 0.25 with 64 x 64
+// ones; the least total wins (64 / 128 / 256: 203 x 4100 x 2080 12 / 16 / 33; 1024 x 4096 x 4096
+// 36 / 27 / 61; 2048 x 4096 x 4096 71 / 43 / 65; 4096 x 15360 x 5120 612 / 369 / 338).
+// Experts: lists of the mean length, each with half a tile to spare.  They are bound by reading
+// the experts' weights until the lists are long: streaming up to four rows a list (64 experts of
+// 4096 x 4096, 4 rows: 172 against 182; 8 rows: 214 against 187), then 128 x 128 tiles against
+// 256 x 256 ones, the smaller tiles only where those leave compute units idle (8 rows: 187
+// against 211 with 64 x 64).
 template <int FW, int FA>
 static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
-    // experts: lists of the mean length, each with half a tile to spare
     const double lists = p.experts ? (double)(p.experts < p.M ? p.experts : p.M) : 1.0, rows = (double)p.M / lists;
-    if (rows <= 16) {
-        const double wgs = lists * (double)p.N;
-        if (wgs >= 64 * 150) return launch_stream<FW, FA, 1, 4, 4, 4>(p, s);
-        if (wgs >= 32 * 150) return launch_stream<FW, FA, 1, 2, 4, 4>(p, s);
-        return launch_stream<FW, FA, 1, 1, 8, 4>(p, s);
+    if (rows <= (p.experts ? 4 : 16)) {
+        const double columns = lists * (double)p.N;
+        if (columns >= 64 * 150) return launch_stream<FW, FA, 1, 4, 4, 2>(p, s);
+        if (columns >= 32 * 150) return launch_stream<FW, FA, 1, 2, 4, 2>(p, s);
+        return launch_stream<FW, FA, 1, 1, 4, 2>(p, s);
     }
-    if (rows <= 64) return launch_stream<FW, FA, 2, 2, 4, 3>(p, s);
     auto tiles = [&](int b) {
-        const double m = p.experts ? lists * (rows / b + 0.5) : (double)((p.M + b - 1) / b);
+        const double m = p.experts ? lists * std::fmax(1.0, rows / b + 0.5) : (double)((p.M + b - 1) / b);
         return m * (double)((p.N + b - 1) / b);
     };
-    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t64 = 0.5 * std::ceil(tiles(64) / 512);
-    const double t128 = tiles(128) <= 256 ? 0.85 : 1.15 * std::ceil(tiles(128) / 512);
-    if (t256 <= t128 && t256 <= t64) return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
-    if (t128 <= t64) return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
-    return launch_tiles<FW, FA, 64, 64, 2, 2, 4>(p, s);
+    auto steps = [&](int b, double one, double two) { return tiles(b) <= 256 ? one : two * std::ceil(tiles(b) / 512); };
+    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t128 = steps(128, 0.7, 1.2), t64 = steps(64, 0.25, 0.48);
+    const bool small = t64 < t128 && !(p.experts && tiles(128) > 256);
+    if (t256 <= t128 && !(small && t64 < t256)) return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
+    if (small) return launch_tiles<FW, FA, 64, 64, 2, 2, 2, 2>(p, s);
+    if (tiles(128) <= 256) return launch_tiles<FW, FA, 128, 128, 2, 2, 2, 2>(p, s);
+    return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
 }
 
 hipError_t launch_gemm_block(const BlockGemmParams& in, hipStream_t s) {

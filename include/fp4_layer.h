@@ -122,8 +122,9 @@ typedef struct {
 /* Y[m, n] = T,  T = sum over the blocks b of 128 columns of K, in order, of
  *   T = fma(P_b[m, n], fl32(a_scales[m, b] * w_scales[n / 128, b]), T),
  * P_b the block's sum of code products on the f8f6f4 matrix cores in binary32 (within
- * fp4_gemm's W8A8 tolerance of the exact value); few rows may be summed as several
- * ranges of K that are then added in order.  The result does not depend on timing.
+ * fp4_gemm's W8A8 tolerance of the exact value); small products may be summed as several
+ * parts of K (ranges, or every so many blocks) that are then added in order.  The result
+ * does not depend on timing; which parts depends on the sizes.
  * Rows of a and w shorter than 4 MiB (lda, ldw), else FP4_ERR_UNSUPPORTED. */
 fp4_status fp4_gemm_block(const fp4_gemm_block_desc* d, void* stream);
 
