@@ -1,13 +1,38 @@
-// Products of 8-bit operands whose scales change along K:
+// Products of 8-bit operands whose scales change along K, and the experts' products:
 //   Y[m, n] = T,  T = fma(P_b[m, n], fl32(sa[m, b] * sw[n / 128, b]), T) over the blocks b
 // of 128 columns of K, P_b = sum over the block of the code products on the f8f6f4 matrix
 // cores.  The scales differ from block to block, so a block's sum cannot stay in the
-// accumulator of the next: every block ends in one fused multiply-add per output value.
+// accumulator of the next: every block ends in one fused multiply-add per output value, and
+// T has to be in vector registers (the accumulation registers take no such instruction).
 //
-// The weight tile is the instruction's first operand, so a lane of a 32 x 32 result holds
-// 16 columns n of one row m: both scales are one value per lane and block, and four
-// consecutive columns leave in one store.
+// The weight tile is the instruction's first operand, so a lane of a result holds columns n
+// of one row m: both scales are one value per lane and block, and four consecutive columns
+// leave in one store.
+//
+// Tile kernel (block_gemm_tile_kernel).  256 x 256 outputs on 8 wavefronts of 128 x 64: T takes
+// 128 of a lane's 256 registers, the most that leaves two wavefronts per SIMD.  Operands go
+// HBM -> LDS without registers, whole 128-byte lines (8 rows x 128 bytes an instruction), two
+// stages of 128 codes; a stage's weights are replaced once every wavefront has them in
+// registers, its activations at the step's end.  Scales come in chunks of 8 blocks: fetched one
+// block at a time, each instruction touched 64 lines and they were a third of all L1 requests.
+// 4096 x 15360 x 5120: 350 us (1.84 PFLOP/s; 8192^3 at 2.2), where the library's product with one
+// scale per tensor reaches 2.9 PFLOP/s at 8192^3.  Bound by LDS: a step (2048 cycles of matrix
+// instructions per SIMD) reads 192 KB of fragments and writes 64 KB, and each 1 KB read costs
+// the SIMD's matrix cores about 18 cycles; the folds add about 500.  Measured at 8192^3 with parts
+// left out: 505 us whole, 430 without loads, 370 without loads and folds.
+// Smaller tiles and two wavefront groups per tile fill the chip on smaller grids (see
+// launch_formats); there a compute unit's load rate (57-70 GB/s) and the latency of a step bound.
+//
+// Streaming kernel (block_gemm_stream_kernel), few rows: bound by reading W.  1 x 11008 x 4096
+// 11.1 us (4.1 TB/s with the launch), 1 x 15360 x 5120 14.2 us (5.5 TB/s), the 64 experts of 8
+// tokens (881 MB) 124-136 us (6.5-7 TB/s).
+//
+// Experts: the list of slots (sorted by expert) is cut into m-tiles expert by expert, a
+// workgroup finds its own from the offsets, and rows are gathered by the loads themselves.
+// 4096 tokens x 8 of 64 experts, 4096 x 5120: 898 us (1.53 PFLOP/s): as above, with a mean of half
+// a tile unused per expert and the weights' 1.3 GB read beside.
 #include <cmath>
+#include <type_traits>
 
 #include "fp4_device.h"
 #include "layer_internal.h"
@@ -306,68 +331,75 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
         load_a(q, q * STAGE);
     }
     step_barrier<(S - 1) * GROUP>();
-    uint32_t cur = 0;
-    for (int b = 0; b < steps; b++) {
-        const uint8_t* sa = smem + cur;
-        const uint8_t* sb = sa + SA;
-        const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) % NCH) * CH);
-        const int c8 = b & 7;
-        const float sw = sc[BM * 8 + (wn * NT * 32) / 128 * 8 + c8];
-        i32x8 w[NT][2];
+    // LIVE m-tiles of each wavefront have rows
+    auto run = [&](auto live) {
+        constexpr int LIVE = decltype(live)::value;
+        uint32_t cur = 0;
+        for (int b = 0; b < steps; b++) {
+            const uint8_t* sa = smem + cur;
+            const uint8_t* sb = sa + SA;
+            const float* sc = reinterpret_cast<const float*>(smem_s + ((b >> 3) % NCH) * CH);
+            const int c8 = b & 7;
+            const float sw = sc[BM * 8 + (wn * NT * 32) / 128 * 8 + c8];
+            i32x8 w[NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; j++)
+            for (int j = 0; j < NT; j++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) w[j][h] = frag(sb, (wn * NT + j) * 32, h);
-        i32x8 a[2];
+                for (int h = 0; h < 2; h++) w[j][h] = frag(sb, (wn * NT + j) * 32, h);
+            i32x8 a[2];
 #pragma unroll
-        for (int h = 0; h < 2; h++) a[h] = frag(sa, wm * 32, h);
-        f32x16 c[NT];
-        float s[MT];
+            for (int h = 0; h < 2; h++) a[h] = frag(sa, wm * 32, h);
+            f32x16 c[NT];
+            float s[LIVE];
 #pragma unroll
-        for (int i = 0; i < MT; i++) s[i] = sc[((i * WM + wm) * 32 + r32) * 8 + (c8 ^ (((i * WM + wm) * 4 + (r32 >> 3)) & 7))] * sw;
-        // m-tile i: the first halves of its NT block sums, then the second; a sum is folded
-        // into t while the matrix cores work on the next one
-        auto fold = [&](int i, int j) {
+            for (int i = 0; i < LIVE; i++) s[i] = sc[((i * WM + wm) * 32 + r32) * 8 + (c8 ^ (((i * WM + wm) * 4 + (r32 >> 3)) & 7))] * sw;
+            // m-tile i: the first halves of its NT block sums, then the second; a sum is folded
+            // into t while the matrix cores work on the next one
+            auto fold = [&](int i, int j) {
 #pragma unroll
-            for (int v = 0; v < 16; v++) t[i][j][v] = __builtin_fmaf(c[j][v], s[i], t[i][j][v]);
-        };
+                for (int v = 0; v < 16; v++) t[i][j][v] = __builtin_fmaf(c[j][v], s[i], t[i][j][v]);
+            };
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            if (i == 1 && MT > 2) {
-                // every wavefront has read this stage's weights: those S steps on replace them
-                step_barrier<S * GROUP>();
-                load_rest(b, cur);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (i + 1 == MT) {
-                // every fragment of this stage is read (by all wavefronts, past the barrier)
-                // and the next stage's loads have landed
-                if constexpr (MT > 2) {
-                    step_barrier<(S - 2) * GROUP + LB + 1>();
-                } else {
-                    step_barrier<(S - 2) * GROUP>();
+            for (int i = 0; i < LIVE; i++) {
+                if (i == 1 && LIVE > 2) {
+                    // every wavefront has read this stage's weights: those S steps on replace them
+                    step_barrier<S * GROUP>();
                     load_rest(b, cur);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                load_a(b + S, cur);
+                if (i + 1 == LIVE) {
+                    // every fragment of this stage is read (by all wavefronts, past the barrier)
+                    // and the next stage's loads have landed
+                    if constexpr (LIVE > 2) {
+                        step_barrier<(S - 2) * GROUP + LB + 1>();
+                    } else {
+                        step_barrier<(S - 2) * GROUP>();
+                        load_rest(b, cur);
+                    }
+                    load_a(b + S, cur);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    if (i > 0 && j + 1 == NT) fold(i - 1, NT - 1);
+                    c[j] = mfma64<FW, FA>(w[j][0], a[0], f32x16{});
+                }
+                if (i + 1 < LIVE) a[0] = frag(sa, ((i + 1) * WM + wm) * 32, 0);
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    c[j] = mfma64<FW, FA>(w[j][1], a[1], c[j]);
+                    if (j > 0) fold(i, j - 1);
+                }
+                if (i + 1 < LIVE) a[1] = frag(sa, ((i + 1) * WM + wm) * 32, 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int j = 0; j < NT; j++) {
-                if (i > 0 && j + 1 == NT) fold(i - 1, NT - 1);
-                c[j] = mfma64<FW, FA>(w[j][0], a[0], f32x16{});
-            }
-            if (i + 1 < MT) a[0] = frag(sa, ((i + 1) * WM + wm) * 32, 0);
-#pragma unroll
-            for (int j = 0; j < NT; j++) {
-                c[j] = mfma64<FW, FA>(w[j][1], a[1], c[j]);
-                if (j > 0) fold(i, j - 1);
-            }
-            if (i + 1 < MT) a[1] = frag(sa, ((i + 1) * WM + wm) * 32, 1);
-            __builtin_amdgcn_sched_barrier(0);
+            fold(LIVE - 1, NT - 1);
+            cur = cur + STAGE == S * STAGE ? 0 : cur + STAGE;
         }
-        fold(MT - 1, NT - 1);
-        cur = cur + STAGE == S * STAGE ? 0 : cur + STAGE;
-    }
+    };
+    // an expert's last tile is half empty as often as not
+    if (EXP && MT > 2 && tile.hi - tile.m0 <= BM / 2) run(std::integral_constant<int, MT / 2 + (MT < 2)>{});
+    else run(std::integral_constant<int, MT>{});
     step_barrier<0>();  // no load into LDS outlives the workgroup
 
     if constexpr (KG > 1) {

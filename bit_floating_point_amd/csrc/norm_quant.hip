@@ -1,10 +1,16 @@
 // Rows of activations to 8-bit codes: the residual addition with the root-mean-square
 // norm, SwiGLU, and the 128 x 128 blocks of weights.
 //
-// All three are one pass over HBM.  A lane owns 8 consecutive columns (one 16-byte load
-// of bf16, two of binary32, one 8-byte store of codes); a row stays in registers between
-// its reduction and its output, so every value is read once.  Sums, statistics and
-// scales are binary32; codes round once, from binary32.
+// All three are one pass over HBM, which bounds them.  A lane owns 8 consecutive columns (one
+// 16-byte load of bf16, two of binary32, one 8-byte store of codes); a row stays in registers
+// between its reduction and its output, so every value is read once.  Inputs are read
+// nontemporally (nothing reads them again).  Sums, statistics and scales are binary32; codes
+// round once, from binary32.
+//
+// Measured (us, bytes of inputs and outputs over time): norm of 4096 x 5120 with eight
+// weighted bf16 terms, residual, codes per 128 and bf16 rows 87 (5.5 TB/s); with one term and no
+// rows 35 (4.2); 777 x 11016 f32 with a static scale 30 (3.7); one row of 5120 3.6 in the kernel, 8
+// with the call.  SwiGLU 4096 x 13824 48 (5.9 TB/s).  A copy on this card reaches 4.8 TB/s, reads 6.
 #include <type_traits>
 
 #include "fp4_device.h"

@@ -10,7 +10,11 @@
 // counts of at most 256 ranges of tokens; every workgroup that places slots adds up the ranges
 // before its own.  The order does not depend on timing.  Few tokens: one workgroup does all.
 //
-// Bound by the vector instructions of the selection.
+// Bound by the vector instructions of the selection: 16384 tokens of 256 experts in 8 groups
+// 28 us, 16 of them the choice (a round of the top_k is about 20 instructions: six fused maxima
+// across the lanes, the winner's lane by a ballot, the lists' shift by bitwise selects; float
+// maxima, which canonicalize, and array selects took 20) and 9 the placement.  One token of 64
+// experts: 4.2 us in the kernel, 6.5 with the call.
 #include "fp4_device.h"
 #include "layer_internal.h"
 
