@@ -433,6 +433,45 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
                     }
     }
 
+    if (p.y_bf16 && p.y_vec8) {
+        // The stages are free now: each wavefront turns its results to rows in LDS of its own
+        // and writes 16 bytes per lane, whole lines of several rows at a time.  (Stores of
+        // four columns straight from the results touch 32 rows an instruction: 4 us more per
+        // 256 x 256 tile.)
+        constexpr int COLS = NT * 32, PITCH = COLS * 2 + 16, LANES = COLS / 8, ROWS = 64 / LANES;
+        // behind the other groups' sums, which slower wavefronts may still be reading
+        constexpr int PARTS = (KG - 1) * NW * MT * NT * 4 * 64 * 16;
+        static_assert(PARTS + NW * MT * 32 * PITCH <= KG * REGION, "the wavefronts' rows fit the stages");
+        uint8_t* mine = smem_all + PARTS + wave * (MT * 32 * PITCH);
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    *reinterpret_cast<bf16x4*>(mine + (i * 32 + r32) * PITCH + (j * 32 + 8 * q + 4 * hk) * 2) =
+                        bf16x4{(__bf16)t[i][j][4 * q], (__bf16)t[i][j][4 * q + 1], (__bf16)t[i][j][4 * q + 2], (__bf16)t[i][j][4 * q + 3]};
+        const int64_t col = n0 + wn * COLS + (lane % LANES) * 8;
+#pragma unroll 4
+        for (int r0 = 0; r0 < MT * 32; r0 += ROWS) {
+            const int r = r0 + lane / LANES;
+            int64_t src = 0;
+            const int64_t out = rows_of(((r >> 5) * WM + wm) * 32 + (r & 31), src);
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + r * PITCH + (lane % LANES) * 16);
+            if (out < 0) continue;
+            __bf16* y = reinterpret_cast<__bf16*>(p.y) + out * p.ldy + col;
+            if (col + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(y) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (col + e < p.N) reinterpret_cast<uint16_t*>(y)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < MT; i++) {
         int64_t src = 0;
@@ -632,6 +671,7 @@ static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
 hipError_t launch_gemm_block(const BlockGemmParams& in, hipStream_t s) {
     BlockGemmParams p = in;
     p.y_vec = p.ldy % 4 == 0;
+    p.y_vec8 = p.ldy % 8 == 0;
     if (p.fw == 0) return p.fa == 0 ? launch_formats<0, 0>(p, s) : launch_formats<0, 1>(p, s);
     return p.fa == 0 ? launch_formats<1, 0>(p, s) : launch_formats<1, 1>(p, s);
 }

@@ -406,6 +406,24 @@ def test_product_strides(M, dtype):
     assert (y[M:] == 5).all() and (y[:, N:] == 5).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 200, 1040), (300, 328, 272), (1030, 1000, 400), (4100, 2056, 144), (4200, 4104, 272)])
+def test_product_wide_rows(M, N, K):
+    """bf16 rows that take 16-byte stores, with a cut last piece: equal to the rounded f32 rows,
+    nothing written past them, on each tile size."""
+    say("product wide rows", M, N, K)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M)
+    a = (torch.randn(M, K, device=DEV, generator=g) * 20).to(torch.float8_e4m3fn).view(torch.uint8)
+    w = (torch.randn(N, K, device=DEV, generator=g) * 20).to(torch.float8_e4m3fn).view(torch.uint8)
+    sa, sw = torch.rand(M, -(-K // 128), device=DEV, generator=g), torch.rand(-(-N // 128), -(-K // 128), device=DEV, generator=g)
+    for n in (N, N - 3):
+        f = F.fp4_gemm_block(a, sa, w[:n], sw[:-(-n // 128)], grid("e4m3"), grid("e4m3"), y_dtype=torch.float32)
+        y = torch.full((M + 1, N + 24), 5.0, dtype=torch.bfloat16, device=DEV)
+        F.fp4_gemm_block(a, sa, w[:n], sw[:-(-n // 128)], grid("e4m3"), grid("e4m3"), y=y[:M, :n])
+        assert torch.equal(y[:M, :n], f.bfloat16())
+        assert (y[M:] == 5).all() and (y[:, n:] == 5).all()
+
+
 def test_product_past_32_bits():
     """Operands, and an output, of more than 2 GiB."""
     for M, N, K in ((560000, 40, 4096), (40, 560000, 4096), (70000, 33000, 128)):
