@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
         if (r < BM) scale_row[r] = rows_of(r, src) < 0 ? kOOB : (uint32_t)(src * p.lda_s * 4);
         else scale_row[r] = src < nbs ? (uint32_t)(src * p.ldw_s * 4) : kOOB;
     }
-    __syncthreads();
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
     const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
     const uint32_t lds_scale = __builtin_amdgcn_readfirstlane(lds + S * STAGE + wave * 256);
@@ -321,13 +320,16 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
         load_w(b + S, stage);
         load_scales(((b + S - 1) >> 3) + 1, (b + S - 1) & 7);
     };
+    load_w(0, 0);
+    load_a(0, 0);
+    __syncthreads();  // the table of scale rows
 #pragma unroll
     for (int c = 0; c < 8; c++) load_scales(0, c);
     // (every stage but the first brings GROUP loads, as in the loop: the waits count them)
 #pragma unroll
-    for (int q = 0; q < S; q++) {
+    for (int q = 1; q < S; q++) {
         load_w(q, q * STAGE);
-        if (q > 0) load_scales(1, q - 1);
+        load_scales(1, q - 1);
         load_a(q, q * STAGE);
     }
     step_barrier<(S - 1) * GROUP>();

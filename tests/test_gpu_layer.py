@@ -406,6 +406,35 @@ def test_product_strides(M, dtype):
     assert (y[M:] == 5).all() and (y[:, N:] == 5).all()
 
 
+def device_operand(g, rows, K, name, lead=()):
+    """As operand(), on the GPU."""
+    v = (torch.randn(*lead, rows, K, device=DEV, generator=g) * 20).clamp(-QMAX[name], QMAX[name]).to(FLOAT8[name])
+    return v.view(torch.uint8), v.double()
+
+
+def device_scales(g, *shape):
+    s = torch.exp2(3 * torch.randn(*shape, device=DEV, generator=g)) * 1e-3
+    return s.masked_fill(torch.rand(*shape, device=DEV, generator=g) < 0.02, 0.0)
+
+
+# Long K (several chunks of scales, a cut last block) on each kernel and tile size, every output
+# checked; the reference in 64 bits on the GPU.
+@pytest.mark.parametrize("M,N,K", [(5, 300, 7184), (16, 5000, 2576), (14, 9700, 3344), (90, 500, 7184), (1500, 2300, 2832),
+                                   (1900, 2500, 2576), (3000, 3100, 3344), (2100, 4400, 1168)])
+def test_product_large(M, N, K):
+    say("product large", M, N, K)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M)
+    a, av = device_operand(g, M, K, "e4m3")
+    w, wv = device_operand(g, N, K, "e4m3")
+    sa, sw = device_scales(g, M, -(-K // 128)), device_scales(g, -(-N // 128), -(-K // 128))
+    ref, S = product_reference(av, sa, wv, sw)
+    y = F.fp4_gemm_block(a, sa, w, sw, grid("e4m3"), grid("e4m3"), y_dtype=torch.float32)
+    check_product(y, ref.cpu(), S.cpu(), K)
+    for _ in range(3):
+        assert torch.equal(F.fp4_gemm_block(a, sa, w, sw, grid("e4m3"), grid("e4m3")), y.bfloat16())
+
+
 @pytest.mark.parametrize("M,N,K", [(70, 200, 1040), (300, 328, 272), (1030, 1000, 400), (4100, 2056, 144), (4200, 4104, 272)])
 def test_product_wide_rows(M, N, K):
     """bf16 rows that take 16-byte stores, with a cut last piece: equal to the rounded f32 rows,
@@ -624,6 +653,38 @@ def test_experts(per, rows, E, k, N, K, skew):
     yb = torch.full((S, N), 7.0, dtype=torch.bfloat16, device=DEV)
     F.fp4_gemm_experts(*args, slots_per_row=k if per == k else 1, y=yb)
     assert torch.equal(yb, y.bfloat16())
+
+
+# Lists from empty to long on each kernel and tile size, long K.
+@pytest.mark.parametrize("T,E,k,N,K,shared", [(2, 40, 6, 500, 2576, True), (30, 24, 4, 700, 2576, False), (200, 12, 3, 1300, 2832, True),
+                                              (1000, 8, 2, 2500, 2576, True), (2000, 6, 2, 3000, 1168, False),
+                                              (3000, 10, 3, 2000, 2576, True)])
+def test_experts_large(T, E, k, N, K, shared):
+    say("experts large", T, E, k, N, K)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    l = torch.randn(T, E, device=DEV, generator=g) + torch.randn(E, device=DEV, generator=g)
+    l[:, 1] = -math.inf
+    l[::50] = math.nan
+    r = F.fp4_route(l, k)
+    rows = T if shared else T * k
+    a, av = device_operand(g, rows, K, "e4m3")
+    w, wv = device_operand(g, N, K, "e4m3", (E,))
+    sa, sw = device_scales(g, rows, -(-K // 128)), device_scales(g, E, -(-N // 128), -(-K // 128))
+    y = torch.full((T * k, N), 7.0, device=DEV)
+    F.fp4_gemm_experts(a, sa, w, sw, grid("e4m3"), grid("e4m3"), r.offsets, r.slots, slots_per_row=k if shared else 1, y=y)
+    choice = r.experts.view(-1)
+    for e in range(E):
+        s = torch.nonzero(choice == e).view(-1)
+        if len(s):
+            src = s // k if shared else s
+            ref, S_ = product_reference(av[src], sa[src], wv[e], sw[e])
+            check_product(y[s], ref.cpu(), S_.cpu(), K)
+    assert (y[choice < 0] == 7).all()
+    for _ in range(3):
+        yb = torch.full((T * k, N), 7.0, dtype=torch.bfloat16, device=DEV)
+        F.fp4_gemm_experts(a, sa, w, sw, grid("e4m3"), grid("e4m3"), r.offsets, r.slots, slots_per_row=k if shared else 1, y=yb)
+        assert torch.equal(yb, y.bfloat16())
 
 
 def test_experts_formats_and_strides():
