@@ -15,8 +15,9 @@
 // stages of 128 codes; a stage's weights are replaced once every wavefront has them in
 // registers, its activations at the step's end.  Scales come in chunks of 8 blocks: fetched one
 // block at a time, each instruction touched 64 lines and they were a third of all L1 requests.
-// 4096 x 15360 x 5120: 350 us (1.84 PFLOP/s; 8192^3 at 2.2), where the library's product with one
-// scale per tensor reaches 2.9 PFLOP/s at 8192^3.  Bound by LDS: a step (2048 cycles of matrix
+// 4096 x 15360 x 5120: 331 us (1.95 PFLOP/s; 8192^3 at 2.2), where the library's product with one
+// scale per tensor reaches 2.9 PFLOP/s at 8192^3; about 8 us of the 82 of a tile are its first
+// loads and its output.  Bound by LDS: a step (2048 cycles of matrix
 // instructions per SIMD) reads 192 KB of fragments and writes 64 KB, and each 1 KB read costs
 // the SIMD's matrix cores about 18 cycles; the folds add about 500.  Measured at 8192^3 with parts
 // left out: 505 us whole, 430 without loads, 370 without loads and folds.
@@ -25,12 +26,13 @@
 //
 // Streaming kernel (block_gemm_stream_kernel), few rows: bound by reading W.  1 x 11008 x 4096
 // 11.1 us (4.1 TB/s with the launch), 1 x 15360 x 5120 14.2 us (5.5 TB/s), the 64 experts of 8
-// tokens (881 MB) 124-136 us (6.5-7 TB/s).
+// tokens (881 MB) 124-138 us (6.4-7 TB/s).
 //
 // Experts: the list of slots (sorted by expert) is cut into m-tiles expert by expert, a
 // workgroup finds its own from the offsets, and rows are gathered by the loads themselves.
-// 4096 tokens x 8 of 64 experts, 4096 x 5120: 898 us (1.53 PFLOP/s): as above, with a mean of half
-// a tile unused per expert and the weights' 1.3 GB read beside.
+// 4096 tokens x 8 of 64 experts, 4096 x 5120: 855 us (1.6 PFLOP/s): as above, with part of each
+// expert's last tile unused (one that is half empty computes half: 898 -> 875 us) and the weights'
+// 1.3 GB read beside.
 #include <cmath>
 #include <type_traits>
 
@@ -638,11 +640,13 @@ static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
 // Up to 16 rows the streaming kernel, as wide in N as leaves 150 workgroups: A is read once per
 // workgroup (16 / 32 / 64 columns: 5120 x 5120, one row 11.6 / 7.7 / 12.4; 11008 x 4096: 13.8 /
 // 11.3 / 11.1; 4096 x 13824, four rows 12.6 / 18.4 / 30.3).  At 17 rows and more the tiles win
-// (24 x 11008 x 4096: 15.0 against 15.9; 64 x 5120 x 5120 on the streaming kernel 14.6 against 13.3).
+// (24 x 11008 x 4096: 13.5 against 15.9).
 // Tiles: a step of 128 of K takes about 2.0 us with a 256 x 256 tile on every compute unit, 1.2
-// with two 128 x 128 ones, 0.7 with one (two groups of wavefronts), 0.48 and 0.25 with 64 x 64
-// ones; the least total wins (64 / 128 / 256: 203 x 4100 x 2080 12 / 16 / 33; 1024 x 4096 x 4096
-// 36 / 27 / 61; 2048 x 4096 x 4096 71 / 43 / 65; 4096 x 15360 x 5120 612 / 369 / 338).
+// with two 128 x 128 ones, 0.7 with one (two groups of wavefronts), 0.44 with two 64 x 64 ones
+// (two groups each) and 0.22 with one (four groups: 64 x 4096 x 4096 10.5 against 11.4 with two,
+// but 203 x 4100 x 2080, 260 tiles, 16.9 against 11.4); the least total wins (64 / 128 / 256:
+// 203 x 4100 x 2080 11 / 16 / 33; 1024 x 4096 x 4096 33 / 25 / 52; 2048 x 4096 x 4096 66 / 41 / 59;
+// 4096 x 15360 x 5120 604 / 390 / 356).
 // Experts: lists of the mean length, each with half a tile to spare.  They are bound by reading
 // the experts' weights until the lists are long: streaming up to four rows a list (64 experts of
 // 4096 x 4096, 4 rows: 172 against 182; 8 rows: 214 against 187), then 128 x 128 tiles against
@@ -662,10 +666,11 @@ static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
         return m * (double)((p.N + b - 1) / b);
     };
     auto steps = [&](int b, double one, double two) { return tiles(b) <= 256 ? one : two * std::ceil(tiles(b) / 512); };
-    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t128 = steps(128, 0.7, 1.2), t64 = steps(64, 0.25, 0.48);
+    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t128 = steps(128, 0.7, 1.2), t64 = steps(64, 0.22, 0.44);
     const bool small = t64 < t128 && !(p.experts && tiles(128) > 256);
     if (t256 <= t128 && !(small && t64 < t256)) return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
-    if (small) return launch_tiles<FW, FA, 64, 64, 2, 2, 2, 2>(p, s);
+    if (small && tiles(64) <= 256) return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 4>(p, s);
+    if (small) return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 2>(p, s);
     if (tiles(128) <= 256) return launch_tiles<FW, FA, 128, 128, 2, 2, 2, 2>(p, s);
     return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
 }

@@ -85,8 +85,9 @@ typedef struct {
 } fp4_swiglu8_desc;
 
 /* h = (g / (1 + e^-g)) u in binary32, g = x[:, 0:cols], u = x[:, cols:2 cols]; codes and
- * scales of h as fp4_rmsnorm_quant's of n.  e^-g and the division are the hardware's
- * (relative error below 2^-21 for |g| <= 80). */
+ * scales of h as fp4_rmsnorm_quant's of n.  e^-g is 2^(-g log2 e), it and the reciprocal are
+ * the hardware's: h is within (2 |g| + 8) 2^-24 of its exact value, relative, and within
+ * 2^-100 |u| for gates below -87, where e^-g may overflow. */
 fp4_status fp4_swiglu_quant(const fp4_swiglu8_desc* d, void* stream);
 
 /* ---- weights with a scale per block of 128 x 128 ---------------------------------- */
@@ -152,8 +153,7 @@ typedef struct {
     int32_t* slots;             /* int32 [tokens * top_k], or NULL with offsets       */
 } fp4_route_desc;
 
-/* Workspace bytes that fp4_route needs for these sizes (0 for few tokens, or without the
- * layout). */
+/* Workspace bytes that fp4_route's layout needs for these sizes (0 for few tokens). */
 size_t fp4_route_workspace_size(int64_t tokens, int32_t experts, int32_t top_k);
 
 /* For every token t, over its usable experts -- those whose logit is finite; infinite
