@@ -57,6 +57,16 @@ __device__ __forceinline__ f32x4 mfma128(i32x8 w, i32x8 a, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, FW, FA, 0, 127, 0, 127);
 }
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+// One store of v at an address that is aligned to ALIGN bytes only: the rows of y start where
+// ldy puts them, and global stores take any alignment.
+template <int ALIGN, typename T>
+__device__ __forceinline__ void store_any(void* at, T v) {
+    struct __attribute__((packed, aligned(ALIGN))) Loose { T v; };
+    reinterpret_cast<Loose*>(at)->v = v;
+}
+
 // four consecutive columns of a row, of which those below N are written
 __device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d);
 
@@ -66,19 +76,18 @@ __device__ __forceinline__ void store_y(const BlockGemmParams& p, int64_t row, i
 }
 
 __device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d) {
-    if (p.y_vec && col + 4 <= p.N) {
+    if (col + 4 <= p.N) {
         const int64_t at = row * p.ldy + col;
         if (p.y_bf16) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p.y) + at) = bf16x4{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
+            const bf16x4 v = {(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
+            store_any<2>(reinterpret_cast<__bf16*>(p.y) + at, __builtin_bit_cast(uint2, v));
         } else {
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.y) + at) = make_float4(a, b, c, d);
+            store_any<4>(reinterpret_cast<float*>(p.y) + at, make_float4(a, b, c, d));
         }
     } else {
         if (col < p.N) store_y(p, row, col, a);
         if (col + 1 < p.N) store_y(p, row, col + 1, b);
         if (col + 2 < p.N) store_y(p, row, col + 2, c);
-        if (col + 3 < p.N) store_y(p, row, col + 3, d);
     }
 }
 
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
                     }
     }
 
-    if (p.y_bf16 && p.y_vec8) {
+    if (p.y_bf16) {
         // The stages are free now: each wavefront turns its results to rows in LDS of its own
         // and writes 16 bytes per lane, whole lines of several rows at a time.  (Stores of
         // four columns straight from the results touch 32 rows an instruction: 4 us more per
@@ -447,7 +456,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
         constexpr int PARTS = (KG - 1) * NW * MT * NT * 4 * 64 * 16;
         static_assert(PARTS + NW * MT * 32 * PITCH <= KG * REGION, "the wavefronts' rows fit the stages");
         uint8_t* mine = smem_all + PARTS + wave * (MT * 32 * PITCH);
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
         for (int i = 0; i < MT; i++)
 #pragma unroll
@@ -466,7 +474,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
             if (out < 0) continue;
             __bf16* y = reinterpret_cast<__bf16*>(p.y) + out * p.ldy + col;
             if (col + 8 <= p.N) {
-                *reinterpret_cast<uint4*>(y) = v;
+                store_any<2>(y, v);
             } else {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -675,10 +683,7 @@ static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
     return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
 }
 
-hipError_t launch_gemm_block(const BlockGemmParams& in, hipStream_t s) {
-    BlockGemmParams p = in;
-    p.y_vec = p.ldy % 4 == 0;
-    p.y_vec8 = p.ldy % 8 == 0;
+hipError_t launch_gemm_block(const BlockGemmParams& p, hipStream_t s) {
     if (p.fw == 0) return p.fa == 0 ? launch_formats<0, 0>(p, s) : launch_formats<0, 1>(p, s);
     return p.fa == 0 ? launch_formats<1, 0>(p, s) : launch_formats<1, 1>(p, s);
 }

@@ -90,7 +90,6 @@ struct BlockGemmParams {
     void* y;
     int64_t ldy;
     int32_t y_bf16;
-    int32_t y_vec, y_vec8;  // rows of y take four, eight values at a time
     int32_t fa, fw;  // matrix-core format codes: 0 E4M3, 1 E5M2
     int32_t experts;
     int32_t slots_per_row;

@@ -11,9 +11,9 @@
 // before its own.  The order does not depend on timing.  Few tokens: one workgroup does all.
 //
 // Bound by the vector instructions of the selection: 16384 tokens of 256 experts in 8 groups
-// 28 us, 16 of them the choice (a round of the top_k is about 20 instructions: six fused maxima
+// 27.5 us, 16 of them the choice (a round of the top_k is about 20 instructions: six fused maxima
 // across the lanes, the winner's lane by a ballot, the lists' shift by bitwise selects; float
-// maxima, which canonicalize, and array selects took 20) and 9 the placement.  One token of 64
+// maxima, which canonicalize, and array selects took 20) and 8 the placement.  One token of 64
 // experts: 4.2 us in the kernel, 6.5 with the call.
 #include "fp4_device.h"
 #include "layer_internal.h"
@@ -25,7 +25,10 @@ namespace {
 constexpr int kNone = INT32_MIN;    // key of an expert that cannot be chosen
 constexpr int kMaxE = 1024;
 constexpr int kRanges = 256;        // ranges of tokens counted apart, at most
-constexpr int kSmallSlots = 1024, kSmallTokens = 64;  // one workgroup routes and places these
+// one workgroup routes and places these, two tokens a wavefront (64 tokens of 64 experts: 12.0 us
+// against 10.3 with two kernels)
+constexpr int kSmallSlots = 1024, kSmallTokens = 32;
+constexpr int kKept = 128;           // slots of a wavefront that the placement keeps in LDS
 constexpr float kLog2e = 0x1.715476p+0f;
 
 // Keys are compared as integers in the order of their floats (-0 as 0): one instruction per
@@ -118,6 +121,8 @@ struct Lane {
     }
 };
 
+constexpr int values_per_load(int epl) { return epl % 4 == 0 ? 4 : epl % 2 == 0 ? 2 : 1; }
+
 // this lane's logits of token t (`whole`: its run is one aligned load)
 template <int EPL>
 __device__ __forceinline__ void load_logits(const RouteParams& p, const Lane<EPL>& me, int64_t t, bool whole, float (&v)[EPL]) {
@@ -126,7 +131,7 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, const Lane<EPL
         for (int i = 0; i < EPL; i++) v[i] = INFINITY;
         if (me.count == EPL) {
             const int64_t at = t * p.ld + me.base;
-            constexpr int W = EPL < 4 ? EPL : 4;  // values per load
+            constexpr int W = values_per_load(EPL);
             if (p.logits_bf16) {
                 struct alignas(2 * W) Part { uint16_t v[W]; };
                 const Part* q = reinterpret_cast<const Part*>(reinterpret_cast<const uint16_t*>(p.logits) + at);
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(1024) route_kernel(RouteParams p, int per_rang
 // Slots of `ranges` consecutive ranges per workgroup (16 wavefronts).
 __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nranges, int ranges, int64_t range_slots, int stride) {
     __shared__ int before[kMaxE + 1], total[kMaxE + 1], chunk[16];
-    __shared__ int part[16][kMaxE + 1];
+    __shared__ int part[16][kMaxE + 1], list[16][kKept];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.experts;
     for (int e = tid; e <= E; e += 1024) before[e] = total[e] = 0;
     for (int e = lane; e <= E; e += 64) part[wave][e] = 0;
@@ -327,7 +332,13 @@ __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nr
         const int e = p.experts_out[s];
         return e < 0 ? E : e;
     };
-    for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&part[wave][expert(s)], 1);
+    // a short list's experts stay in LDS: read once, on their way beside the counts
+    const bool kept = quota <= kKept;
+    int mine[kKept / 64];
+    if (kept) {
+#pragma unroll
+        for (int i = 0; i < kKept / 64; i++) mine[i] = w0 + 64 * i + lane < w1 ? expert(w0 + 64 * i + lane) : -1;
+    }
     int sum = 0;
     for (int e = lane * 4; e < stride; e += 256) {
         int4 all = make_int4(0, 0, 0, 0), b = all;
@@ -350,6 +361,15 @@ __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nr
     }
     sum = scan64(sum);
     if (lane == 63) atomicSub(&before[E], sum);
+    if (kept) {
+#pragma unroll
+        for (int i = 0; i < kKept / 64; i++) {
+            list[wave][64 * i + lane] = mine[i];
+            if (mine[i] >= 0) atomicAdd(&part[wave][mine[i]], 1);
+        }
+    } else {
+        for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&part[wave][expert(s)], 1);
+    }
     __syncthreads();
     exclusive(total, chunk, E + 1);
     for (int e = tid; e <= E; e += 1024) {
@@ -364,7 +384,8 @@ __global__ void __launch_bounds__(1024) route_place_kernel(RouteParams p, int nr
         }
     }
     __syncthreads();
-    place(p, w0, w1, part[wave], lane, expert);
+    if (kept) place(p, w0, w1, part[wave], lane, [&](int64_t s) { return list[wave][s - w0]; });
+    else place(p, w0, w1, part[wave], lane, expert);
 }
 
 // Few tokens: choice and layout in one workgroup (16 wavefronts).
@@ -436,8 +457,9 @@ size_t route_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k) {
 template <int EPL>
 static hipError_t launch_choice(const RouteParams& p, int lg_bits, hipStream_t s) {
     // whether every lane's run of experts is whole and aligned for one load (of 16 bytes at most)
-    const int size = p.experts / p.groups, bytes = (p.logits_bf16 ? 2 : 4) * (EPL < 4 ? EPL : 4);
-    const bool whole = EPL > 1 && size % EPL == 0 && p.ld % EPL == 0 && reinterpret_cast<uintptr_t>(p.logits) % bytes == 0;
+    constexpr int W = values_per_load(EPL);
+    const int size = p.experts / p.groups, bytes = (p.logits_bf16 ? 2 : 4) * W;
+    const bool whole = W > 1 && size % EPL == 0 && p.ld % W == 0 && reinterpret_cast<uintptr_t>(p.logits) % bytes == 0;
 
     if (route_small(p.tokens, p.top_k)) {
         const int waves = p.offsets || p.tokens >= 16 ? 16 : (int)p.tokens;
@@ -468,8 +490,11 @@ hipError_t launch_route(const RouteParams& p, hipStream_t s) {
     const int lanes = 1 << lg_bits, epl = (p.experts / p.groups + lanes - 1) / lanes;
     if (epl <= 1) return launch_choice<1>(p, lg_bits, s);
     if (epl <= 2) return launch_choice<2>(p, lg_bits, s);
+    if (epl <= 3) return launch_choice<3>(p, lg_bits, s);
     if (epl <= 4) return launch_choice<4>(p, lg_bits, s);
+    if (epl <= 6) return launch_choice<6>(p, lg_bits, s);
     if (epl <= 8) return launch_choice<8>(p, lg_bits, s);
+    if (epl <= 12) return launch_choice<12>(p, lg_bits, s);
     if (epl <= 16) return launch_choice<16>(p, lg_bits, s);
     return launch_choice<32>(p, lg_bits, s);
 }

@@ -558,7 +558,9 @@ def check_routing(got, want, E):
     (33, 1000, 5, "sigmoid", False, 1, 1, 1, True, "bf16"), (500, 128, 8, "sigmoid", True, 4, 2, 2, True, "f32"),
     (5000, 16, 2, "softmax", False, 1, 1, 1, True, "f32"), (2500, 72, 6, "sigmoid", True, 9, 4, 2, True, "f32"),
     (300, 96, 3, "softmax", True, 32, 5, 2, True, "f32"), (150, 512, 8, "sigmoid", True, 16, 4, 2, True, "f32"),
-    (700, 64, 8, "sigmoid", False, 64, 8, 1, False, "f32"), (90, 33, 32, "softmax", False, 1, 1, 1, True, "f32")])
+    (700, 64, 8, "sigmoid", False, 64, 8, 1, False, "f32"), (90, 33, 32, "softmax", False, 1, 1, 1, True, "f32"),
+    (50, 700, 8, "softmax", False, 1, 1, 1, True, "f32"), (45, 768, 6, "sigmoid", True, 1, 1, 1, True, "bf16"),
+    (20, 1023, 8, "softmax", False, 33, 5, 1, True, "f32"), (120, 192, 8, "sigmoid", True, 8, 3, 2, True, "f32")])
 def test_route(T, E, k, score, biased, groups, top_groups, group_top, renorm, dtype):
     say("route", T, E, k, score, biased, groups, top_groups, group_top)
     g = rng(T + E)
