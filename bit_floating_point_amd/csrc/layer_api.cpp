@@ -23,16 +23,24 @@ fp4_status fp8_grid(const fp4_grid& g, QGrid* q) {
     return FP4_OK;
 }
 
+// `count` rows or matrices `stride` elements apart (both >= 0) have byte offsets of 64 bits
+fp4_status spans(const char* name, int64_t count, int64_t stride) {
+    if (!below(count, stride, 1ll << 60)) return report(FP4_ERR_UNSUPPORTED, "%s spans more than 2^60 elements", name);
+    return FP4_OK;
+}
+
 // the matrix [rows, cols] at p: leading dimension and alignment of 16-byte accesses
-fp4_status matrix(const char* name, const void* p, int64_t ld, int64_t cols, int32_t type) {
+fp4_status matrix(const char* name, const void* p, int64_t rows, int64_t ld, int64_t cols, int32_t type) {
     if (ld < cols) return report(FP4_ERR_INVALID_ARG, "leading dimension of %s below its columns", name);
+    fp4_status st = spans(name, rows, ld);
+    if (st) return st;
     if (!aligned(p, 16) || (ld * size_of(type)) % 16 != 0)
         return report(FP4_ERR_ALIGNMENT, "%s must be 16-byte aligned, its rows a multiple of 16 bytes apart", name);
     return FP4_OK;
 }
 
 // codes and scales of rows of `cols` values; *out is filled in
-fp4_status code_output(int64_t cols, const fp4_grid& grid, const fp4_gran& gran, const float* tensor_scale,
+fp4_status code_output(int64_t rows, int64_t cols, const fp4_grid& grid, const fp4_gran& gran, const float* tensor_scale,
                        const int8_t* col_shift, uint8_t* packed, int64_t ldp, void* scales, CodeOut* out) {
     QGrid q;
     fp4_status st = fp8_grid(grid, &q);
@@ -52,6 +60,7 @@ fp4_status code_output(int64_t cols, const fp4_grid& grid, const fp4_gran& gran,
     if (gran.mode == FP4_SCALE_GROUP && (gran.group < 8 || gran.group > 512 || (gran.group & (gran.group - 1))))
         return report(FP4_ERR_UNSUPPORTED, "group must be a power of two in [8, 512] (got %d)", gran.group);
     if (ldp < cols) return report(FP4_ERR_INVALID_ARG, "ldp below the code bytes of a row");
+    if ((st = spans("packed", rows, ldp))) return st;
     if (!aligned(packed, 8) || ldp % 8 != 0 || !aligned(col_shift, 8))
         return report(FP4_ERR_ALIGNMENT, "packed and col_shift must be 8-byte aligned, ldp a multiple of 8");
     if (!aligned(tensor_scale, 4) || !aligned(scales, gran.scale_dtype == FP4_F16 ? 2 : 4))
@@ -98,14 +107,16 @@ fp4_status product_sizes(int64_t M, int64_t N, int64_t K) {
     return FP4_OK;
 }
 
-fp4_status product_output(const void* y, int64_t ldy, int64_t N, int32_t type) {
+fp4_status product_output(const void* y, int64_t M, int64_t ldy, int64_t N, int32_t type) {
     if (!float_type(type)) return report(FP4_ERR_INVALID_ARG, "y_dtype must be FP4_F32 or FP4_BF16");
     if (ldy < N) return report(FP4_ERR_INVALID_ARG, "ldy below N");
+    fp4_status st = spans("y", M, ldy);
+    if (st) return st;
     if (!aligned(y, 16)) return report(FP4_ERR_ALIGNMENT, "y must be 16-byte aligned");
     return FP4_OK;
 }
 
-int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+int64_t blocks_of(int64_t n) { return n / kBlock + (n % kBlock != 0); }
 
 }  // namespace
 
@@ -125,14 +136,14 @@ fp4_status fp4_rmsnorm_quant(const fp4_rmsnorm_desc* d, void* stream) {
     if (empty) return report_ok();
     if (!d->x || !d->gamma) return report(FP4_ERR_INVALID_ARG, "null pointer");
     NormParams p{};
-    if (d->packed && (st = code_output(d->cols, d->grid, d->gran, d->tensor_scale, d->col_shift, d->packed, d->ldp, d->scales, &p.out)))
+    if (d->packed && (st = code_output(d->rows, d->cols, d->grid, d->gran, d->tensor_scale, d->col_shift, d->packed, d->ldp, d->scales, &p.out)))
         return st;
-    if ((st = matrix("x", d->x, d->ldx, d->cols, d->x_dtype))) return st;
-    if (d->residual && (st = matrix("residual", d->residual, d->ldr, d->cols, d->residual_dtype))) return st;
-    if (d->residual_out && (st = matrix("residual_out", d->residual_out, d->ldro, d->cols, d->residual_dtype))) return st;
+    if ((st = matrix("x", d->x, d->rows, d->ldx, d->cols, d->x_dtype))) return st;
+    if (d->residual && (st = matrix("residual", d->residual, d->rows, d->ldr, d->cols, d->residual_dtype))) return st;
+    if (d->residual_out && (st = matrix("residual_out", d->residual_out, d->rows, d->ldro, d->cols, d->residual_dtype))) return st;
     if (d->residual_out && d->residual_out == d->residual && d->ldro != d->ldr)
         return report(FP4_ERR_INVALID_ARG, "residual_out may be residual only with the same leading dimension");
-    if (d->y && (st = matrix("y", d->y, d->ldy, d->cols, d->y_dtype))) return st;
+    if (d->y && (st = matrix("y", d->y, d->rows, d->ldy, d->cols, d->y_dtype))) return st;
     if (!aligned(d->gamma, 16) || !aligned(d->term_weights, 4))
         return report(FP4_ERR_ALIGNMENT, "gamma must be 16-byte aligned, term_weights 4-byte aligned");
     p.rows = d->rows;
@@ -165,8 +176,8 @@ fp4_status fp4_swiglu_quant(const fp4_swiglu8_desc* d, void* stream) {
     if (d->rows == 0 || d->cols == 0) return report_ok();
     if (!d->x || !d->packed) return report(FP4_ERR_INVALID_ARG, "null pointer");
     SwigluParams p{};
-    if ((st = code_output(d->cols, d->grid, d->gran, d->tensor_scale, d->col_shift, d->packed, d->ldp, d->scales, &p.out))) return st;
-    if ((st = matrix("x", d->x, d->ldx, 2 * d->cols, d->x_dtype))) return st;
+    if ((st = code_output(d->rows, d->cols, d->grid, d->gran, d->tensor_scale, d->col_shift, d->packed, d->ldp, d->scales, &p.out))) return st;
+    if ((st = matrix("x", d->x, d->rows, d->ldx, 2 * d->cols, d->x_dtype))) return st;
     p.rows = d->rows;
     p.cols = d->cols;
     p.x = d->x;
@@ -186,8 +197,9 @@ fp4_status fp4_quantize_block(const void* w, int32_t w_dtype, int64_t batch, int
     if (st) return st;
     if (batch == 0 || n == 0 || k == 0) return report_ok();
     if (!w || !packed || !scales) return report(FP4_ERR_INVALID_ARG, "null pointer");
-    if ((st = matrix("w", w, ldw, k, w_dtype))) return st;
+    if ((st = matrix("w", w, n, ldw, k, w_dtype))) return st;
     if (ldp < k || stride_w < 0 || stride_p < 0) return report(FP4_ERR_INVALID_ARG, "bad leading dimension or stride");
+    if ((st = spans("packed", n, ldp)) || (st = spans("w", batch, stride_w)) || (st = spans("packed", batch, stride_p))) return st;
     if (!aligned(packed, 8) || ldp % 8 != 0 || stride_p % 8 != 0 || (stride_w * size_of(w_dtype)) % 16 != 0 || !aligned(scales, 4))
         return report(FP4_ERR_ALIGNMENT, "packed, ldp and stride_p must be multiples of 8 bytes, stride_w of 16");
     if (!below(batch, blocks_of(n), 0x80000000ll) || !below(batch * blocks_of(n), blocks_of(k), 0x80000000ll))
@@ -217,7 +229,7 @@ fp4_status fp4_gemm_block(const fp4_gemm_block_desc* d, void* stream) {
     if (d->reserved != 0) return report(FP4_ERR_INVALID_ARG, "reserved must be 0");
     if ((st = code_operand("a", d->a, d->lda, d->K, d->a_grid, &p.fa))) return st;
     if ((st = code_operand("w", d->w, d->ldw, d->K, d->w_grid, &p.fw))) return st;
-    if ((st = product_output(d->y, d->ldy, d->N, d->y_dtype))) return st;
+    if ((st = product_output(d->y, d->M, d->ldy, d->N, d->y_dtype))) return st;
     if (d->lda_s < blocks_of(d->K) || d->ldw_s < blocks_of(d->K))
         return report(FP4_ERR_INVALID_ARG, "leading dimension of scales below ceil(K / 128)");
     if (d->lda_s > (1 << 20) || d->ldw_s > (1 << 20)) return report(FP4_ERR_UNSUPPORTED, "rows of scales must be shorter than 4 MiB");
@@ -255,6 +267,8 @@ fp4_status fp4_route(const fp4_route_desc* d, void* workspace, size_t ws_bytes, 
         return report(FP4_ERR_UNSUPPORTED, "top_k must be 1..32 and at most the experts (got %d)", d->top_k);
     if (d->tokens < 0 || !below(d->tokens, d->top_k, 0x80000000ll) || d->ld < d->experts)
         return report(FP4_ERR_INVALID_ARG, "bad sizes tokens=%lld ld=%lld", (long long)d->tokens, (long long)d->ld);
+    fp4_status st = spans("logits", d->tokens, d->ld);
+    if (st) return st;
     if (!float_type(d->logits_dtype)) return report(FP4_ERR_INVALID_ARG, "logits_dtype must be FP4_F32 or FP4_BF16");
     if (d->score != FP4_ROUTE_SOFTMAX && d->score != FP4_ROUTE_SIGMOID) return report(FP4_ERR_INVALID_ARG, "bad score %d", d->score);
     if (d->groups < 1 || d->groups > 64 || d->experts % d->groups != 0 || d->top_groups < 1 || d->top_groups > d->groups)
@@ -303,11 +317,12 @@ fp4_status fp4_gemm_experts(const fp4_gemm_experts_desc* d, void* stream) {
     if (d->slots_per_row < 1) return report(FP4_ERR_INVALID_ARG, "slots_per_row must be positive");
     if ((st = code_operand("a", d->a, d->lda, d->K, d->a_grid, &p.fa))) return st;
     if ((st = code_operand("w", d->w, d->ldw, d->K, d->w_grid, &p.fw))) return st;
-    if ((st = product_output(d->y, d->ldy, d->N, d->y_dtype))) return st;
+    if ((st = product_output(d->y, d->slots, d->ldy, d->N, d->y_dtype))) return st;
     if (d->lda_s > (1 << 20)) return report(FP4_ERR_UNSUPPORTED, "rows of scales must be shorter than 4 MiB");
     if (d->lda_s < blocks_of(d->K)) return report(FP4_ERR_INVALID_ARG, "leading dimension of scales below ceil(K / 128)");
     if (d->stride_w < 0) return report(FP4_ERR_INVALID_ARG, "bad stride between experts");
     if (d->stride_w % 16 != 0) return report(FP4_ERR_ALIGNMENT, "experts must be a multiple of 16 bytes apart");
+    if ((st = spans("w", d->experts, d->stride_w))) return st;
     if (d->slots == 0 || d->N == 0) return report_ok();
     if (!d->a || !d->a_scales || !d->w || !d->w_scales || !d->y || !d->offsets || !d->slot_list)
         return report(FP4_ERR_INVALID_ARG, "null pointer");
