@@ -112,6 +112,8 @@ __device__ __forceinline__ uint2 codes8(const float v[8]) {
 }
 __device__ __forceinline__ uint2 codes8(const float y[8], bool e4m3) { return e4m3 ? codes8<true>(y) : codes8<false>(y); }
 
+constexpr float kLargest = 0x1.fffffep+127f;  // a factor past it would turn zeros into NaN
+
 // fl32(1 / s), 0 for s = 0: the hardware's reciprocal and one Newton step, which is the
 // correctly rounded value wherever neither is subnormal (checked for every significand)
 __device__ __forceinline__ float reciprocal(float s) {
@@ -119,8 +121,13 @@ __device__ __forceinline__ float reciprocal(float s) {
         const float r = __builtin_amdgcn_rcpf(s);
         return __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
     }
-    return recip_or_zero(s);
+    return fminf(recip_or_zero(s), kLargest);
 }
+
+// The least scale of a unit with a value that is not 0: the smallest normal number.  Below
+// 2^-128 a scale has no binary32 reciprocal; with this one such values keep their codes'
+// absolute precision, half the smallest code's value times 2^-126.
+constexpr float kLeastScale = 0x1p-126f;
 
 // A unit's scale s = fl32(amax / Qmax), rounded to binary16 where scales are stored so: a
 // product and a correction, correctly rounded unless subnormal (checked likewise).
@@ -130,7 +137,7 @@ __device__ __forceinline__ float unit_scale(float amax, const CodeOut& o) {
         const float q = amax * o.rqmax;
         s = __builtin_fmaf(__builtin_fmaf(-q, o.qmax, amax), o.rqmax, q);
     } else {
-        s = amax / o.qmax;
+        s = amax > 0.0f ? fmaxf(amax / o.qmax, kLeastScale) : 0.0f;
     }
     return o.scale_f16 ? round_f16(s) : s;
 }
@@ -147,13 +154,14 @@ __device__ __forceinline__ void store_codes8(const CodeOut& o, int64_t row, int6
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int sh = (int)(int8_t)((i < 4 ? k.x : k.y) >> (8 * (i & 3)));
-            y[i] = v[i] * ldexpf(r, -sh);
+            y[i] = v[i] * fminf(ldexpf(r, -sh), kLargest);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = v[i] * r;
     }
-    // a unit's own binary32 scale keeps its values within half a step of Qmax
+    // a unit's own binary32 scale (never below kLeastScale) keeps its values within half a step
+    // of Qmax; a given scale does not, nor one that binary16 rounded
     if (o.mode == 0 || o.scale_f16) {
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(y[i], -o.qmax, o.qmax);
@@ -369,7 +377,8 @@ __global__ void __launch_bounds__(256) quantize_block_kernel(BlockQuantParams p,
         if (row < p.n && col < p.k) get8(p.w, BF16, m * p.stride_w + row * p.ldw + col, v[i]);
         amax = fmaxf(amax, amax8(v[i]));
     }
-    const float s = block_max(amax, part, 4) / p.qmax;
+    const float top = block_max(amax, part, 4);
+    const float s = top > 0.0f ? fmaxf(top / p.qmax, kLeastScale) : 0.0f;
     if (threadIdx.x == 0) p.scales[b] = s;
     const float r = recip_or_zero(s);
 #pragma unroll

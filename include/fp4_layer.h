@@ -61,9 +61,11 @@ typedef struct {
  *       row of x is read as zeros whatever it holds.
  *   n = (h / sqrt(mean(h^2) + eps)) * gamma, everything in binary32
  *   residual_out = h, y = n, each rounded to its type
- *   codes of n: per unit (row or group) s = fl32(amax / Qmax) (rounded to binary16 for
- *       f16 scales), codes of fl32(n * fl32(1/s)) as fp4_quantize_pack; with TENSOR the
- *       given scale and shifts, codes of fl32(n * fl32(1/s) 2^-k).
+ *   codes of n: per unit (row or group) s = fl32(amax / Qmax), no less than 2^-126 unless
+ *       amax is 0 (rounded to binary16 for f16 scales), codes of fl32(n * fl32(1/s)) as
+ *       fp4_quantize_pack; with TENSOR the given scale and shifts, codes of
+ *       fl32(n * fl32(1/s) 2^-k), a factor past binary32 being its largest number.  Zeros
+ *       have the codes of zero whatever the scale.
  * At least one of packed, y, residual_out is given.  Several terms are an expert layer's
  * outputs (one row per token and chosen expert, fp4_route's weights) joining the stream. */
 fp4_status fp4_rmsnorm_quant(const fp4_rmsnorm_desc* d, void* stream);
@@ -93,7 +95,8 @@ fp4_status fp4_swiglu_quant(const fp4_swiglu8_desc* d, void* stream);
 /* ---- weights with a scale per block of 128 x 128 ---------------------------------- */
 /* For each of `batch` matrices w[b] = w + b * stride_w elements, [n, k] with leading dim
  * ldw: every block of 128 rows and 128 columns (the last ones shorter) gets
- * s = fl32(amax / Qmax) and the codes of fl32(w * fl32(1/s)).
+ * s = fl32(amax / Qmax), no less than 2^-126 unless amax is 0, and the codes of
+ * fl32(w * fl32(1/s)).
  *   w_dtype  FP4_F32 or FP4_BF16; k a multiple of 8
  *   packed   codes [batch][n, k], leading dim ldp bytes, matrices stride_p bytes apart
  *   scales   f32 [batch, ceil(n / 128), ceil(k / 128)] contiguous                     */
