@@ -616,32 +616,55 @@ __global__ void __launch_bounds__(64 * KS, 2) block_gemm_stream_kernel(BlockGemm
     }
 }
 
+// launch(part, grid_m, grid_n) for the product, in as few parts as launches allow: ranges of
+// column blocks that begin on a scale block of W, and for dense operands of row blocks.
+// (Experts: tiles_m is the most that any layout takes, and stays below a launch's limit.)
+template <int BM, int BN, typename Launch>
+static hipError_t in_parts(const BlockGemmParams& p, int64_t tiles_m, int threads, Launch launch) {
+    constexpr int64_t U = BN < kBlock ? kBlock / BN : 1;  // column blocks of a scale block
+    const int64_t most = max_workgroups(threads), tiles_n = (p.N + BN - 1) / BN;
+    const int64_t fit = most / (tiles_n < U ? tiles_n : U), gm = p.experts || tiles_m < fit ? tiles_m : fit;
+    const int64_t gn = tiles_n <= most / gm ? tiles_n : most / gm / U * U;
+    for (int64_t m = 0; m < tiles_m; m += gm) {
+        for (int64_t n = 0; n < tiles_n; n += gn) {
+            BlockGemmParams q = p;
+            const int64_t row = m * BM, col = n * BN, tm = tiles_m - m < gm ? tiles_m - m : gm, tn = tiles_n - n < gn ? tiles_n - n : gn;
+            if (!p.experts) q.M = p.M - row < tm * BM ? p.M - row : tm * BM;
+            q.N = p.N - col < tn * BN ? p.N - col : tn * BN;
+            q.a += row * p.lda;
+            q.a_scales += row * p.lda_s;
+            q.w += col * p.ldw;
+            q.w_scales += col / kBlock * p.ldw_s;
+            q.y = reinterpret_cast<uint8_t*>(p.y) + (row * p.ldy + col) * (p.y_bf16 ? 2 : 4);
+            launch(q, tm, tn);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+// m-tiles of BM rows: those of the experts' lists however the slots fall
+static int64_t m_tiles(const BlockGemmParams& p, int64_t bm) {
+    return p.experts ? p.M / bm + (p.experts < p.M ? p.experts : p.M) : (p.M + bm - 1) / bm;
+}
+
 template <int FW, int FA, int MT, int NT, int KS, int D>
 static hipError_t launch_stream(const BlockGemmParams& p, hipStream_t s) {
-    const int64_t grid_n = (p.N + 16 * NT - 1) / (16 * NT);
-    if (p.experts) {
-        const int64_t most = p.M / (16 * MT) + (p.experts < p.M ? p.experts : p.M);
-        block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, true><<<(unsigned)(most * grid_n), 64 * KS, 0, s>>>(p, 0, (int)grid_n);
-    } else {
-        const int64_t grid_m = (p.M + 16 * MT - 1) / (16 * MT);
-        block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, false>
-            <<<(unsigned)(grid_m * grid_n), 64 * KS, 0, s>>>(p, (int)grid_m, (int)grid_n);
-    }
-    return hipGetLastError();
+    constexpr int threads = 64 * KS;
+    return in_parts<16 * MT, 16 * NT>(p, m_tiles(p, 16 * MT), threads, [&](const BlockGemmParams& q, int64_t gm, int64_t gn) {
+        if (q.experts) block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, true><<<(unsigned)(gm * gn), threads, 0, s>>>(q, 0, (int)gn);
+        else block_gemm_stream_kernel<FW, FA, MT, NT, KS, D, false><<<(unsigned)(gm * gn), threads, 0, s>>>(q, (int)gm, (int)gn);
+    });
 }
 
 template <int FW, int FA, int BM, int BN, int WM, int WN, int S, int KG = 1>
 static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
-    const int64_t grid_n = (p.N + BN - 1) / BN;
-    if (p.experts) {
-        const int64_t most = p.M / BM + (p.experts < p.M ? p.experts : p.M);  // m-tiles, however the slots fall
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, true><<<(unsigned)(most * grid_n), 64 * WM * WN * KG, 0, s>>>(p, 0, (int)grid_n);
-    } else {
-        const int64_t grid_m = (p.M + BM - 1) / BM;
-        block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, false>
-            <<<(unsigned)(grid_m * grid_n), 64 * WM * WN * KG, 0, s>>>(p, (int)grid_m, (int)grid_n);
-    }
-    return hipGetLastError();
+    constexpr int threads = 64 * WM * WN * KG;
+    return in_parts<BM, BN>(p, m_tiles(p, BM), threads, [&](const BlockGemmParams& q, int64_t gm, int64_t gn) {
+        if (q.experts) block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, true><<<(unsigned)(gm * gn), threads, 0, s>>>(q, 0, (int)gn);
+        else block_gemm_tile_kernel<FW, FA, BM, BN, WM, WN, S, KG, false><<<(unsigned)(gm * gn), threads, 0, s>>>(q, (int)gm, (int)gn);
+    });
 }
 
 // Which kernel (us, measured one against the other).

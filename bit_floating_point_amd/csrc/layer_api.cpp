@@ -315,6 +315,9 @@ fp4_status fp4_gemm_experts(const fp4_gemm_experts_desc* d, void* stream) {
     if (d->reserved != 0) return report(FP4_ERR_INVALID_ARG, "reserved must be 0");
     if (d->experts < 1 || d->experts > 1024) return report(FP4_ERR_UNSUPPORTED, "1 to 1024 experts (got %d)", d->experts);
     if (d->slots_per_row < 1) return report(FP4_ERR_INVALID_ARG, "slots_per_row must be positive");
+    // the tiles of rows have to fit one launch (2^23 - 1 of 256 rows); every expert may have one
+    // that is partly filled
+    if (d->slots >= (1ll << 31) - (1 << 18)) return report(FP4_ERR_UNSUPPORTED, "slots must be below 2^31 - 2^18 (got %lld)", (long long)d->slots);
     if ((st = code_operand("a", d->a, d->lda, d->K, d->a_grid, &p.fa))) return st;
     if ((st = code_operand("w", d->w, d->ldw, d->K, d->w_grid, &p.fw))) return st;
     if ((st = product_output(d->y, d->slots, d->ldy, d->N, d->y_dtype))) return st;

@@ -19,6 +19,10 @@ fp4_status grid_table(const fp4_grid& g, QGrid* q);
 
 constexpr int kBlock = 128;  // rows and columns of a scale block
 
+// Workgroups of one launch: its threads number less than 2^32.  Past that the grid wraps and the
+// rest does not run, with no error, so launchers split larger work.
+inline int64_t max_workgroups(int threads) { return 0xffffffffll / threads; }
+
 // where 8-bit codes and their scales go
 struct CodeOut {
     uint8_t* packed;  // null: no codes

@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(256) swiglu_quant_flat_kernel(SwigluParams p, 
 
 // One workgroup per block of 128 x 128: thread t holds 8 columns of rows t / 16 + 16 i.
 template <bool BF16>
-__global__ void __launch_bounds__(256) quantize_block_kernel(BlockQuantParams p, int nb, int kb) {
+__global__ void __launch_bounds__(256) quantize_block_kernel(BlockQuantParams p, int64_t first, int nb, int kb) {
     __shared__ float part[4];
-    const int64_t b = blockIdx.x;
+    const int64_t b = first + blockIdx.x;
     const int64_t kblk = b % kb, nblk = (b / kb) % nb, m = b / ((int64_t)kb * nb);
     const int64_t col = kblk * kBlock + (threadIdx.x & 15) * 8;
     float v[8][8], amax = 0.0f;
@@ -396,6 +396,51 @@ __global__ void __launch_bounds__(256) quantize_block_kernel(BlockQuantParams p,
 // wavefronts of a workgroup that covers `chunks` chunks of 8 columns, nc per thread
 static int waves_for(int64_t chunks, int nc) { return (int)((chunks + 64 * nc - 1) / (64 * nc)); }
 
+// p advanced by `bytes` (null stays null)
+template <typename T>
+static T* ahead(T* p, int64_t bytes) {
+    return p ? reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes) : p;
+}
+
+// the outputs, and the operands, of rows first .. first + rows - 1
+static CodeOut rows_of(const CodeOut& o, int64_t cols, int64_t first) {
+    CodeOut q = o;
+    const int64_t units = o.mode == 1 ? 1 : o.mode == 2 ? (cols + o.group - 1) / o.group : 0;
+    q.packed = ahead(o.packed, first * o.ldp);
+    q.scales = ahead(o.scales, first * units * (o.scale_f16 ? 2 : 4));
+    return q;
+}
+static NormParams rows_of(const NormParams& p, int64_t first, int64_t rows) {
+    NormParams q = p;
+    const int64_t stream = p.residual_bf16 ? 2 : 4;
+    q.rows = rows;
+    q.x = ahead(p.x, first * p.terms * p.ldx * (p.x_bf16 ? 2 : 4));
+    q.term_weights = ahead(p.term_weights, first * p.terms * 4);
+    q.residual = ahead(p.residual, first * p.ldr * stream);
+    q.residual_out = ahead(p.residual_out, first * p.ldro * stream);
+    q.y = ahead(p.y, first * p.ldy * (p.y_bf16 ? 2 : 4));
+    q.out = rows_of(p.out, p.cols, first);
+    return q;
+}
+static SwigluParams rows_of(const SwigluParams& p, int64_t first, int64_t rows) {
+    SwigluParams q = p;
+    q.rows = rows;
+    q.x = ahead(p.x, first * p.ldx * (p.x_bf16 ? 2 : 4));
+    q.out = rows_of(p.out, p.cols, first);
+    return q;
+}
+
+// `launch` on parts of at most `most` rows
+template <typename Params, typename Launch>
+static hipError_t by_rows(const Params& p, int64_t most, Launch launch) {
+    for (int64_t first = 0; first < p.rows; first += most) {
+        launch(p.rows <= most ? p : rows_of(p, first, p.rows - first < most ? p.rows - first : most));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Chunks per thread.  Few rows, whose latency counts: one (64 x 8192 of 8 terms: 9.4 us against
 // 14.9 with two).  Many: with several terms in flight two (4096 x 5120 of 8 terms, one / two /
 // four chunks: 91 / 90 / 98 us), with one term four, so that enough bytes are on their way
@@ -403,17 +448,18 @@ static int waves_for(int64_t chunks, int nc) { return (int)((chunks + 64 * nc - 
 template <bool XBF>
 static hipError_t launch_norm(const NormParams& p, hipStream_t s) {
     const int64_t chunks = (p.cols + 7) / 8;
-    const dim3 grid((unsigned)p.rows);
     // (777 x 11016 f32 of one term: two chunks 28 us, four 32)
     const int few = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
     const int many = chunks <= 256 ? 1 : p.terms > 1 && chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
     const int nc = p.rows < 1024 ? few : many;
     const int threads = 64 * waves_for(chunks, nc);
-    if (nc == 1) rmsnorm_quant_kernel<1, XBF><<<grid, threads, 0, s>>>(p);
-    else if (nc == 2) rmsnorm_quant_kernel<2, XBF><<<grid, threads, 0, s>>>(p);
-    else if (nc == 4) rmsnorm_quant_kernel<4, XBF><<<grid, threads, 0, s>>>(p);
-    else rmsnorm_quant_kernel<8, XBF><<<grid, threads, 0, s>>>(p);
-    return hipGetLastError();
+    return by_rows(p, max_workgroups(threads), [&](const NormParams& q) {
+        const dim3 grid((unsigned)q.rows);
+        if (nc == 1) rmsnorm_quant_kernel<1, XBF><<<grid, threads, 0, s>>>(q);
+        else if (nc == 2) rmsnorm_quant_kernel<2, XBF><<<grid, threads, 0, s>>>(q);
+        else if (nc == 4) rmsnorm_quant_kernel<4, XBF><<<grid, threads, 0, s>>>(q);
+        else rmsnorm_quant_kernel<8, XBF><<<grid, threads, 0, s>>>(q);
+    });
 }
 
 hipError_t launch_rmsnorm_quant(const NormParams& p, hipStream_t s) {
@@ -426,27 +472,35 @@ hipError_t launch_swiglu_quant(const SwigluParams& p, hipStream_t s) {
         // whole groups per row: at least the lanes of a group
         int cbits = p.out.mode == 2 && p.out.group > 8 ? __builtin_ctz(p.out.group / 8) : 0;
         while (cbits < 8 && (1 << cbits) < chunks) cbits++;
-        const int64_t parts = (chunks + (1 << cbits) - 1) >> cbits, rows = (p.rows + (256 >> cbits) - 1) / (256 >> cbits);
-        if (parts * rows <= 0x7fffffff) {
-            if (p.x_bf16) swiglu_quant_flat_kernel<true><<<(unsigned)(parts * rows), 256, 0, s>>>(p, cbits, (uint32_t)parts);
-            else swiglu_quant_flat_kernel<false><<<(unsigned)(parts * rows), 256, 0, s>>>(p, cbits, (uint32_t)parts);
-            return hipGetLastError();
-        }
+        const int64_t parts = (chunks + (1 << cbits) - 1) >> cbits, height = 256 >> cbits;  // of a workgroup, in rows
+        return by_rows(p, max_workgroups(256) / parts * height, [&](const SwigluParams& q) {
+            const unsigned grid = (unsigned)(parts * ((q.rows + height - 1) / height));
+            if (q.x_bf16) swiglu_quant_flat_kernel<true><<<grid, 256, 0, s>>>(q, cbits, (uint32_t)parts);
+            else swiglu_quant_flat_kernel<false><<<grid, 256, 0, s>>>(q, cbits, (uint32_t)parts);
+        });
     }
-    const dim3 grid((unsigned)p.rows);
-    if (chunks <= 256 || (chunks <= 1024 && p.rows < 512)) swiglu_quant_kernel<1><<<grid, 64 * waves_for(chunks, 1), 0, s>>>(p);
-    else if (chunks <= 2048 && p.rows < 512) swiglu_quant_kernel<2><<<grid, 64 * waves_for(chunks, 2), 0, s>>>(p);
-    else if (chunks <= 4096) swiglu_quant_kernel<4><<<grid, 64 * waves_for(chunks, 4), 0, s>>>(p);
-    else swiglu_quant_kernel<8><<<grid, 64 * waves_for(chunks, 8), 0, s>>>(p);
-    return hipGetLastError();
+    const int nc = chunks <= 256 || (chunks <= 1024 && p.rows < 512) ? 1 : chunks <= 2048 && p.rows < 512 ? 2 : chunks <= 4096 ? 4 : 8;
+    const int threads = 64 * waves_for(chunks, nc);
+    return by_rows(p, max_workgroups(threads), [&](const SwigluParams& q) {
+        const dim3 grid((unsigned)q.rows);
+        if (nc == 1) swiglu_quant_kernel<1><<<grid, threads, 0, s>>>(q);
+        else if (nc == 2) swiglu_quant_kernel<2><<<grid, threads, 0, s>>>(q);
+        else if (nc == 4) swiglu_quant_kernel<4><<<grid, threads, 0, s>>>(q);
+        else swiglu_quant_kernel<8><<<grid, threads, 0, s>>>(q);
+    });
 }
 
 hipError_t launch_quantize_block(const BlockQuantParams& p, hipStream_t s) {
     const int64_t nb = (p.n + kBlock - 1) / kBlock, kb = (p.k + kBlock - 1) / kBlock;
-    const dim3 grid((unsigned)(p.batch * nb * kb));
-    if (p.bf16) quantize_block_kernel<true><<<grid, 256, 0, s>>>(p, (int)nb, (int)kb);
-    else quantize_block_kernel<false><<<grid, 256, 0, s>>>(p, (int)nb, (int)kb);
-    return hipGetLastError();
+    const int64_t blocks = p.batch * nb * kb, most = max_workgroups(256);
+    for (int64_t first = 0; first < blocks; first += most) {
+        const unsigned grid = (unsigned)(blocks - first < most ? blocks - first : most);
+        if (p.bf16) quantize_block_kernel<true><<<grid, 256, 0, s>>>(p, first, (int)nb, (int)kb);
+        else quantize_block_kernel<false><<<grid, 256, 0, s>>>(p, first, (int)nb, (int)kb);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace fp4

@@ -178,7 +178,7 @@ fp4_status fp4_route(const fp4_route_desc* d, void* workspace, size_t ws_bytes, 
 
 /* ---- the experts' products ---------------------------------------------------------- */
 typedef struct {
-    int64_t slots;              /* rows of Y; < 2^31                                  */
+    int64_t slots;              /* rows of Y; < 2^31 - 2^18                           */
     int64_t N, K;               /* of each expert; K a multiple of 16                 */
     int32_t experts;            /* 1..1024                                            */
     int32_t slots_per_row;      /* slot s reads row s / slots_per_row of a: top_k for
