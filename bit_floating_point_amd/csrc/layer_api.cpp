@@ -116,6 +116,19 @@ fp4_status product_output(const void* y, int64_t M, int64_t ldy, int64_t N, int3
     return FP4_OK;
 }
 
+// whether two of `batch` matrices of n rows of k bytes, rows ld (>= k) and matrices `stride` bytes
+// apart, share a byte: rows of matrices i and i + d do if d * stride is less than k from a
+// multiple of ld that is below n * ld
+bool overlap(int64_t batch, int64_t n, int64_t k, int64_t ld, int64_t stride) {
+    const int64_t span = (n - 1) * ld + k;
+    if (batch < 2 || stride >= span || (stride >= k && (batch - 1) * stride + k <= ld)) return false;
+    for (int64_t d = 1; d < batch && d * stride < span; d++) {
+        const int64_t rest = d * stride % ld;
+        if (rest < k || (rest > ld - k && d * stride / ld + 1 < n)) return true;
+    }
+    return false;
+}
+
 int64_t blocks_of(int64_t n) { return n / kBlock + (n % kBlock != 0); }
 
 }  // namespace
@@ -200,10 +213,11 @@ fp4_status fp4_quantize_block(const void* w, int32_t w_dtype, int64_t batch, int
     if ((st = matrix("w", w, n, ldw, k, w_dtype))) return st;
     if (ldp < k || stride_w < 0 || stride_p < 0) return report(FP4_ERR_INVALID_ARG, "bad leading dimension or stride");
     if ((st = spans("packed", n, ldp)) || (st = spans("w", batch, stride_w)) || (st = spans("packed", batch, stride_p))) return st;
-    if (!aligned(packed, 8) || ldp % 8 != 0 || stride_p % 8 != 0 || (stride_w * size_of(w_dtype)) % 16 != 0 || !aligned(scales, 4))
-        return report(FP4_ERR_ALIGNMENT, "packed, ldp and stride_p must be multiples of 8 bytes, stride_w of 16");
     if (!below(batch, blocks_of(n), 0x80000000ll) || !below(batch * blocks_of(n), blocks_of(k), 0x80000000ll))
         return report(FP4_ERR_UNSUPPORTED, "more than 2^31 scale blocks");
+    if (overlap(batch, n, k, ldp, stride_p)) return report(FP4_ERR_INVALID_ARG, "the matrices of packed overlap");
+    if (!aligned(packed, 8) || ldp % 8 != 0 || stride_p % 8 != 0 || (stride_w * size_of(w_dtype)) % 16 != 0 || !aligned(scales, 4))
+        return report(FP4_ERR_ALIGNMENT, "packed, ldp and stride_p must be multiples of 8 bytes, stride_w of 16");
     BlockQuantParams p{};
     p.w = w;
     p.bf16 = w_dtype == FP4_BF16;

@@ -215,11 +215,12 @@ def fp4_quantize_block(w: torch.Tensor, grid: L.fp4_grid, packed: torch.Tensor |
         scales = torch.empty((*lead, *blocks), dtype=torch.float32, device=dev)
     _need(packed.shape == w.shape and packed.dtype == torch.uint8 and packed.device == dev, "packed must be uint8 of w's shape")
     _need((w.stride(-1) == 1 and packed.stride(-1) == 1) or k <= 1, "w and packed must be row-major")
+    ldw, ldp = (max(t.stride(-2), k) if n <= 1 else t.stride(-2) for t in (w, packed))
     batch = lead[0] if lead else 1
     _flat(scales, "scales", batch * blocks[0] * blocks[1], torch.float32, dev)
     _check(_call("fp4_quantize_block")(
-        w.data_ptr(), _type(w, "w"), batch, n, k, max(w.stride(-2), k), w.stride(0) if lead else 0, grid, packed.data_ptr(),
-        max(packed.stride(-2), k), packed.stride(0) if lead else 0, scales.data_ptr(), _stream(dev)), "fp4_quantize_block")
+        w.data_ptr(), _type(w, "w"), batch, n, k, ldw, w.stride(0) if lead else 0, grid, packed.data_ptr(),
+        ldp, packed.stride(0) if lead else 0, scales.data_ptr(), _stream(dev)), "fp4_quantize_block")
     return packed, scales
 
 

@@ -98,7 +98,8 @@ fp4_status fp4_swiglu_quant(const fp4_swiglu8_desc* d, void* stream);
  * s = fl32(amax / Qmax), no less than 2^-126 unless amax is 0, and the codes of
  * fl32(w * fl32(1/s)).
  *   w_dtype  FP4_F32 or FP4_BF16; k a multiple of 8
- *   packed   codes [batch][n, k], leading dim ldp bytes, matrices stride_p bytes apart
+ *   packed   codes [batch][n, k], leading dim ldp bytes, matrices stride_p bytes apart, none of
+ *            which share a byte (those of w may)
  *   scales   f32 [batch, ceil(n / 128), ceil(k / 128)] contiguous                     */
 fp4_status fp4_quantize_block(const void* w, int32_t w_dtype, int64_t batch, int64_t n, int64_t k,
                               int64_t ldw, int64_t stride_w, fp4_grid grid, uint8_t* packed,
