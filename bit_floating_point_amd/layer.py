@@ -269,6 +269,8 @@ def fp4_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
         if slots is None:
             slots = torch.empty(T * top_k, dtype=torch.int32, device=dev)
         need = _call("fp4_route_workspace_size")(T, E, top_k)
+        if need and workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous memory on {dev}")
         if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:

@@ -81,3 +81,26 @@ def test_overlap_rule(batch, ldp, stride_p, status):
     got = Y._call("fp4_quantize_block")(0x10000, L.FP4_F32, batch, 64, 256, 256, 64 * 256, E4M3, 0x10000, ldp, stride_p, 0x10002, None)
     assert got == status
     assert (b"overlap" in L.lib().fp4_last_error()) == (status == L.FP4_ERR_INVALID_ARG)
+
+
+# fp4_route counts in the caller's workspace: it has to be memory of the logits' device, as large
+# as it says.
+@pytest.mark.parametrize("workspace", [torch.empty(1 << 20, dtype=torch.uint8, device="meta"),
+                                       torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+                                       torch.zeros(4096, dtype=torch.int32).as_strided((1 << 10, 64), (4, 1)),
+                                       torch.zeros(1 << 20, dtype=torch.uint8)[::2]])
+def test_route_workspace(workspace):
+    with pytest.raises(ValueError, match="workspace"):
+        F.fp4_route(torch.zeros(4096, 64), 8, workspace=workspace)
+
+
+def test_route_takes_a_workspace(monkeypatch):
+    """A workspace that is large enough is used, a small one replaced, none needed for few tokens."""
+    size, given = Y._call("fp4_route_workspace_size"), []
+    monkeypatch.setattr(Y, "_call", lambda name: size if name.endswith("size") else lambda *a: given.append(a) or 0)
+    workspace = torch.zeros(1 << 20, dtype=torch.uint8)
+    F.fp4_route(torch.zeros(4096, 64), 8, workspace=workspace)
+    F.fp4_route(torch.zeros(4096, 64), 8, workspace=workspace[:64])
+    F.fp4_route(torch.zeros(4, 64), 8, workspace=workspace)
+    assert given[0][1] == workspace.data_ptr() and given[0][2] == size(4096, 64, 8)
+    assert given[1][1] != workspace.data_ptr() and given[2][1] is None
