@@ -87,7 +87,7 @@ def test_overlap_rule(batch, ldp, stride_p, status):
 # as it says.
 @pytest.mark.parametrize("workspace", [torch.empty(1 << 20, dtype=torch.uint8, device="meta"),
                                        torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
-                                       torch.zeros(4096, dtype=torch.int32).as_strided((1 << 10, 64), (4, 1)),
+                                       torch.zeros(8192, dtype=torch.int32).as_strided((1 << 10, 64), (4, 1)),
                                        torch.zeros(1 << 20, dtype=torch.uint8)[::2]])
 def test_route_workspace(workspace):
     with pytest.raises(ValueError, match="workspace"):
