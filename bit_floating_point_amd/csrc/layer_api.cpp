@@ -151,7 +151,7 @@ fp4_status fp4_rmsnorm_quant(const fp4_rmsnorm_desc* d, void* stream) {
     NormParams p{};
     if (d->packed && (st = code_output(d->rows, d->cols, d->grid, d->gran, d->tensor_scale, d->col_shift, d->packed, d->ldp, d->scales, &p.out)))
         return st;
-    if ((st = matrix("x", d->x, d->rows, d->ldx, d->cols, d->x_dtype))) return st;
+    if ((st = matrix("x", d->x, d->rows * d->terms, d->ldx, d->cols, d->x_dtype))) return st;
     if (d->residual && (st = matrix("residual", d->residual, d->rows, d->ldr, d->cols, d->residual_dtype))) return st;
     if (d->residual_out && (st = matrix("residual_out", d->residual_out, d->rows, d->ldro, d->cols, d->residual_dtype))) return st;
     if (d->residual_out && d->residual_out == d->residual && d->ldro != d->ldr)

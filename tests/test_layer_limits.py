@@ -21,3 +21,12 @@ def test_experts_slots(slots):
                                 lda_s=2, a_grid=grid(), w=FAKE, ldw=256, stride_w=64 * 256, w_scales=FAKE, w_grid=grid(),
                                 offsets=FAKE, slot_list=FAKE, y=FAKE, ldy=64, y_dtype=L.FP4_BF16)
     assert Y._call("fp4_gemm_experts")(d, None) == L.FP4_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("terms,status", [(1, L.FP4_ERR_ALIGNMENT), (2, L.FP4_ERR_UNSUPPORTED), (64, L.FP4_ERR_UNSUPPORTED)])
+def test_norm_span_of_all_terms(terms, status):
+    """x has rows * terms rows: their byte offsets have to fit 64 bits.  (What passes stops at
+    gamma's alignment.)"""
+    d = Y.fp4_rmsnorm_desc(rows=1 << 24, cols=256, x=FAKE, ldx=(1 << 36) - 64, x_dtype=L.FP4_F32, terms=terms, gamma=FAKE + 4,
+                           gamma_dtype=L.FP4_F32, residual_dtype=L.FP4_BF16, eps=1e-6, y_dtype=L.FP4_BF16, y=FAKE, ldy=256)
+    assert Y._call("fp4_rmsnorm_quant")(d, None) == status
