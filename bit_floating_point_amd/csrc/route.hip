@@ -172,11 +172,13 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const Lan
         rsum = 1.0f / sum64(s);
     }
     // Keys: score + bias; without a bias the logit, which has the scores' order and neither
-    // rounds nor underflows.
+    // rounds nor underflows.  A bias of -inf or NaN takes its expert out.
     if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            key[i] = key[i] == kNone ? kNone : ordered(score_of(logit[i], p.sigmoid, top, rsum) + me.bias[i]);
+        for (int i = 0; i < EPL; i++) {
+            const float v = score_of(logit[i], p.sigmoid, top, rsum) + me.bias[i];
+            key[i] = key[i] != kNone && v > -INFINITY ? ordered(v) : kNone;
+        }
     }
 #pragma unroll
     for (int a = 0; a + 1 < EPL; a++) {  // largest first; equal keys stay in order

@@ -144,7 +144,8 @@ typedef struct {
     int64_t ld;                 /* elements                                           */
     int32_t logits_dtype;       /* FP4_F32 or FP4_BF16 (element-aligned)              */
     int32_t score;              /* FP4_ROUTE_SOFTMAX or FP4_ROUTE_SIGMOID             */
-    const float* bias;          /* f32 [experts] added for the choice only, or NULL   */
+    const float* bias;          /* f32 [experts] added for the choice only, or NULL;
+                                   -inf or NaN: no token may choose the expert        */
     int32_t groups;             /* experts form this many equal groups (1: none), <= 64 */
     int32_t top_groups;         /* groups a token may use, 1..groups                  */
     int32_t group_top;          /* a group's value: the sum of its best 1 or 2 keys   */
@@ -162,7 +163,9 @@ size_t fp4_route_workspace_size(int64_t tokens, int32_t experts, int32_t top_k);
 
 /* For every token t, over its usable experts -- those whose logit is finite; infinite
  * (either sign) and NaN logits mark experts the token may not use:
- *   score = softmax over the usable logits, or 1 / (1 + e^-logit); binary32
+ *   score = softmax over the usable logits, or 1 / (1 + e^-logit); binary32.  (An expert
+ *     whose bias is -inf or NaN has a score, and counts in the softmax, but none of what
+ *     follows chooses it; a bias of +inf comes first.)
  *   groups > 1: a group's value is the sum of its group_top largest score + bias (of fewer,
  *     if fewer are usable); only experts of the top_groups best groups that have a usable
  *     expert stay (ties: the lower group)
