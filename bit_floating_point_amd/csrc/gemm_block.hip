@@ -67,14 +67,12 @@ __device__ __forceinline__ void store_any(void* at, T v) {
     reinterpret_cast<Loose*>(at)->v = v;
 }
 
-// four consecutive columns of a row, of which those below N are written
-__device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d);
-
 __device__ __forceinline__ void store_y(const BlockGemmParams& p, int64_t row, int64_t col, float v) {
     if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[row * p.ldy + col] = (__bf16)v;
     else reinterpret_cast<float*>(p.y)[row * p.ldy + col] = v;
 }
 
+// four consecutive columns of a row, of which those below N are written
 __device__ __forceinline__ void store_y4(const BlockGemmParams& p, int64_t row, int64_t col, float a, float b, float c, float d) {
     if (col + 4 <= p.N) {
         const int64_t at = row * p.ldy + col;
@@ -198,8 +196,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
     constexpr int NW = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
     constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
     // scales: chunks of 8 blocks of K, BM rows (and the column blocks of W) of 8 values
-    constexpr int CH = BM * 32 + 256 * (NW - BM / 64), NCH = S > 2 ? 3 : 2;
+    constexpr int CH = BM * 32 + 256 * (NW - BM / 64), NCH = 2;
     constexpr int LA = SA / 1024 / NW, LB = SB / 1024 / NW;
+    static_assert(S == 2, "the counted waits and the scales' two chunks are for two stages");
     static_assert(BM / 64 < NW, "one wavefront per 64 scales of A, one for those of W");
     constexpr int REGION = S * STAGE + (NCH * CH + 1023) / 1024 * 1024;  // of one group
     __shared__ __attribute__((aligned(1024))) uint8_t smem_all[KG * REGION];
@@ -384,9 +383,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
                     // every fragment of this stage is read (by all wavefronts, past the barrier)
                     // and the next stage's loads have landed
                     if constexpr (LIVE > 2) {
-                        step_barrier<(S - 2) * GROUP + LB + 1>();
+                        step_barrier<LB + 1>();
                     } else {
-                        step_barrier<(S - 2) * GROUP>();
+                        step_barrier<0>();
                         load_rest(b, cur);
                     }
                     load_a(b + S, cur);
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
         }
     };
     // an expert's last tile is half empty as often as not
-    if (EXP && MT > 2 && tile.hi - tile.m0 <= BM / 2) run(std::integral_constant<int, MT / 2 + (MT < 2)>{});
+    if (EXP && MT > 2 && tile.hi - tile.m0 <= BM / 2) run(std::integral_constant<int, MT / 2>{});
     else run(std::integral_constant<int, MT>{});
     step_barrier<0>();  // no load into LDS outlives the workgroup
 

@@ -465,7 +465,7 @@ static hipError_t launch_choice(const RouteParams& p, int lg_bits, hipStream_t s
 
     if (route_small(p.tokens, p.top_k)) {
         const int waves = p.offsets || p.tokens >= 16 ? 16 : (int)p.tokens;
-        route_small_kernel<EPL><<<1, 64 * (p.offsets ? 16 : waves), 0, s>>>(p, lg_bits, whole);
+        route_small_kernel<EPL><<<1, 64 * waves, 0, s>>>(p, lg_bits, whole);
         return hipGetLastError();
     }
     const int64_t per = route_range(p.tokens), nranges = (p.tokens + per - 1) / per;
