@@ -258,8 +258,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) block_gemm_tile_kernel(B
     const i32x4v rsS = of_a ? buf_words(EXP ? p.a_scales : p.a_scales + tile.m0 * p.lda_s, a_rows * p.lda_s * 4)
                             : buf_words(p.w_scales + tile.e * p.stride_ws + nb0 * p.ldw_s, nbs * p.ldw_s * 4);
     const int seg = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
-    // dense operands: one offset per lane, the later pieces by the scalar offset (the range
-    // check includes it, so rows past the operand read zeros)
+    // dense operands: one offset per lane, the later pieces by the scalar offset.  Rows past the
+    // operand read zeros: without a stride or swizzle a buffer's range check covers the sum of
+    // both offsets (out of range where the lane's offset >= num_records - the scalar one: the
+    // CDNA3 instruction set manual, range checking of buffer accesses), also where the scalar
+    // offset alone is past the end.  Measured so on gfx950 for these loads into LDS and for
+    // register loads of 4 and 16 bytes, on a descriptor shorter than its allocation.
     uint32_t offA[EXP ? LA : 1], offB;
     const int r8 = wave * 8 + (lane >> 3);
     if constexpr (EXP) {
