@@ -22,7 +22,7 @@
 // the SIMD's matrix cores about 18 cycles; the folds add about 500.  Measured at 8192^3 with parts
 // left out: 505 us whole, 430 without loads, 370 without loads and folds.
 // Smaller tiles and two wavefront groups per tile fill the chip on smaller grids (see
-// launch_formats); there a compute unit's load rate (57-70 GB/s) and the latency of a step bound.
+// gemm_block_choice.h); there a compute unit's load rate (57-70 GB/s) and the latency of a step bound.
 //
 // Streaming kernel (block_gemm_stream_kernel), few rows: bound by reading W.  1 x 11008 x 4096
 // 11.1 us (4.1 TB/s with the launch), 1 x 15360 x 5120 14.2 us (5.5 TB/s), the 64 experts of 8
@@ -33,10 +33,10 @@
 // 4096 tokens x 8 of 64 experts, 4096 x 5120: 855 us (1.6 PFLOP/s): as above, with part of each
 // expert's last tile unused (one that is half empty computes half: 898 -> 875 us) and the weights'
 // 1.3 GB read beside.
-#include <cmath>
 #include <type_traits>
 
 #include "fp4_device.h"
+#include "gemm_block_choice.h"
 #include "layer_internal.h"
 
 namespace fp4 {
@@ -670,43 +670,19 @@ static hipError_t launch_tiles(const BlockGemmParams& p, hipStream_t s) {
     });
 }
 
-// Which kernel (us, measured one against the other).
-// Up to 16 rows the streaming kernel, as wide in N as leaves 150 workgroups: A is read once per
-// workgroup (16 / 32 / 64 columns: 5120 x 5120, one row 11.6 / 7.7 / 12.4; 11008 x 4096: 13.8 /
-// 11.3 / 11.1; 4096 x 13824, four rows 12.6 / 18.4 / 30.3).  At 17 rows and more the tiles win
-// (24 x 11008 x 4096: 13.5 against 15.9).
-// Tiles: a step of 128 of K takes about 2.0 us with a 256 x 256 tile on every compute unit, 1.2
-// with two 128 x 128 ones, 0.7 with one (two groups of wavefronts), 0.44 with two 64 x 64 ones
-// (two groups each) and 0.22 with one (four groups: 64 x 4096 x 4096 10.5 against 11.4 with two,
-// but 203 x 4100 x 2080, 260 tiles, 16.9 against 11.4); the least total wins (64 / 128 / 256:
-// 203 x 4100 x 2080 11 / 16 / 33; 1024 x 4096 x 4096 33 / 25 / 52; 2048 x 4096 x 4096 66 / 41 / 59;
-// 4096 x 15360 x 5120 604 / 390 / 356).
-// Experts: lists of the mean length, each with half a tile to spare.  They are bound by reading
-// the experts' weights until the lists are long: streaming up to four rows a list (64 experts of
-// 4096 x 4096, 4 rows: 172 against 182; 8 rows: 214 against 187), then 128 x 128 tiles against
-// 256 x 256 ones, the smaller tiles only where those leave compute units idle (8 rows: 187
-// against 211 with 64 x 64).
 template <int FW, int FA>
 static hipError_t launch_formats(const BlockGemmParams& p, hipStream_t s) {
-    const double lists = p.experts ? (double)(p.experts < p.M ? p.experts : p.M) : 1.0, rows = (double)p.M / lists;
-    if (rows <= (p.experts ? 4 : 16)) {
-        const double columns = lists * (double)p.N;
-        if (columns >= 64 * 150) return launch_stream<FW, FA, 1, 4, 4, 2>(p, s);
-        if (columns >= 32 * 150) return launch_stream<FW, FA, 1, 2, 4, 2>(p, s);
-        return launch_stream<FW, FA, 1, 1, 4, 2>(p, s);
+    switch (block_kernel(p.experts, p.M, p.N)) {
+        case BlockKernel::kStream16: return launch_stream<FW, FA, 1, 1, 4, 2>(p, s);
+        case BlockKernel::kStream32: return launch_stream<FW, FA, 1, 2, 4, 2>(p, s);
+        case BlockKernel::kStream64: return launch_stream<FW, FA, 1, 4, 4, 2>(p, s);
+        case BlockKernel::kTile64K4: return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 4>(p, s);
+        case BlockKernel::kTile64K2: return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 2>(p, s);
+        case BlockKernel::kTile128K2: return launch_tiles<FW, FA, 128, 128, 2, 2, 2, 2>(p, s);
+        case BlockKernel::kTile128: return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
+        case BlockKernel::kTile256: break;
     }
-    auto tiles = [&](int b) {
-        const double m = p.experts ? lists * std::fmax(1.0, rows / b + 0.5) : (double)((p.M + b - 1) / b);
-        return m * (double)((p.N + b - 1) / b);
-    };
-    auto steps = [&](int b, double one, double two) { return tiles(b) <= 256 ? one : two * std::ceil(tiles(b) / 512); };
-    const double t256 = 2.0 * std::ceil(tiles(256) / 256), t128 = steps(128, 0.7, 1.2), t64 = steps(64, 0.22, 0.44);
-    const bool small = t64 < t128 && !(p.experts && tiles(128) > 256);
-    if (t256 <= t128 && !(small && t64 < t256)) return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
-    if (small && tiles(64) <= 256) return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 4>(p, s);
-    if (small) return launch_tiles<FW, FA, 64, 64, 1, 2, 2, 2>(p, s);
-    if (tiles(128) <= 256) return launch_tiles<FW, FA, 128, 128, 2, 2, 2, 2>(p, s);
-    return launch_tiles<FW, FA, 128, 128, 2, 2, 2>(p, s);
+    return launch_tiles<FW, FA, 256, 256, 2, 4, 2>(p, s);
 }
 
 hipError_t launch_gemm_block(const BlockGemmParams& p, hipStream_t s) {
