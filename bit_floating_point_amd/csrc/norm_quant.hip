@@ -479,7 +479,13 @@ hipError_t launch_swiglu_quant(const SwigluParams& p, hipStream_t s) {
             else swiglu_quant_flat_kernel<false><<<grid, 256, 0, s>>>(q, cbits, (uint32_t)parts);
         });
     }
-    const int nc = chunks <= 256 || (chunks <= 1024 && p.rows < 512) ? 1 : chunks <= 2048 && p.rows < 512 ? 2 : chunks <= 4096 ? 4 : 8;
+    // Row scales.  Below 1024 rows a row's latency counts: as few chunks per thread as a workgroup
+    // of 1024 covers (one / two / four / eight chunks, us: 512 x 4096 4.8 / 5.6 / 7.6 / 10.8; 512 x
+    // 11008 two 8.2, four 9.8; 64 x 32768 four 8.8, eight 12.3).  With more rows their bytes do: two
+    // up to 8192 columns (4096 x 8192: 34.8 / 31.6 / 32.9 / 36.4; but one for 2048 and less, 1024 x
+    // 2048: 5.1 / 5.8), then four (4096 x 13824 two 60.3, four 54.0, eight 59.6).
+    const int few = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
+    const int nc = p.rows < 1024 || chunks <= 256 || chunks > 4096 ? few : chunks <= 1024 ? 2 : 4;
     const int threads = 64 * waves_for(chunks, nc);
     return by_rows(p, max_workgroups(threads), [&](const SwigluParams& q) {
         const dim3 grid((unsigned)q.rows);
