@@ -11,10 +11,12 @@
 // before its own.  The order does not depend on timing.  Few tokens: one workgroup does all.
 //
 // Bound by the vector instructions of the selection: 16384 tokens of 256 experts in 8 groups
-// 27.5 us, 16 of them the choice (a round of the top_k is about 20 instructions: six fused maxima
-// across the lanes, the winner's lane by a ballot, the lists' shift by bitwise selects; float
-// maxima, which canonicalize, and array selects took 20) and 8 the placement.  One token of 64
-// experts: 4.2 us in the kernel, 6.5 with the call.
+// 26.8 us, about 18 of them the choice, which issues 476 vector instructions a token, 76 % of
+// its cycles on every SIMD (a round of the top_k is about 20: six fused maxima across the lanes,
+// the winner's lane by a ballot, the lists' shift by bitwise selects; float maxima, which
+// canonicalize, and array selects took 4 us more).  The placement's 8 us are launch, the table
+// of counts and the order inside each workgroup.  One token of 64 experts: 4.5 us, 6.2 with the
+// call.
 #include "fp4_device.h"
 #include "layer_internal.h"
 
@@ -25,8 +27,8 @@ namespace {
 constexpr int kNone = INT32_MIN;    // key of an expert that cannot be chosen
 constexpr int kMaxE = 1024;
 constexpr int kRanges = 256;        // ranges of tokens counted apart, at most
-// one workgroup routes and places these, two tokens a wavefront (64 tokens of 64 experts: 12.0 us
-// against 10.3 with two kernels)
+// one workgroup routes and places these, two tokens a wavefront (one workgroup / two kernels, us,
+// 8 of 64 experts: 16 tokens 6.0 / 8.0, 32 8.0 / 8.3, 48 10.1 / 8.5; 8 of 256: 32 tokens 10.2 / 9.8)
 constexpr int kSmallSlots = 1024, kSmallTokens = 32;
 constexpr int kKept = 128;           // slots of a wavefront that the placement keeps in LDS
 constexpr float kLog2e = 0x1.715476p+0f;
@@ -472,8 +474,11 @@ static hipError_t launch_choice(const RouteParams& p, int lg_bits, hipStream_t s
     route_kernel<EPL><<<(unsigned)nranges, 1024, 0, s>>>(p, (int)per, lg_bits, route_stride(p.experts), whole);
     if (p.offsets) {
         const int64_t nslots = p.tokens * p.top_k;
-        int64_t wgs = (nslots + 2047) / 2048;
-        if (wgs > 64) wgs = 64;
+        // A workgroup per 512 slots, of whole ranges (512 / 1024 / 2048 slots with at most 256
+        // workgroups, and 2048 with 64, us for choice and placement: 256 tokens of 64 experts, 8
+        // each, 9.4 / 9.5 / 10.3 / 10.3; 4096 of 256 13.3 / 13.6 / 14.5 / 14.5; 65536 of 64
+        // 44.1 / 44.3 / 44.2 / 50.4).
+        const int64_t wgs = min((nslots + 511) / 512, nranges);
         const int64_t ranges = (nranges + wgs - 1) / wgs;
         route_place_kernel<<<(unsigned)((nranges + ranges - 1) / ranges), 1024, 0, s>>>(p, (int)nranges, (int)ranges, per * p.top_k,
                                                                                            route_stride(p.experts));
