@@ -5,6 +5,11 @@
 // accumulator of the next: every block ends in one fused multiply-add per output value, and
 // T has to be in vector registers (the accumulation registers take no such instruction).
 //
+// Below binary32: within a block the matrix instruction drops product bits under 2^-13 of the
+// largest product of 8, which is what its rate costs.  Binary32 results lie 1.5e-5 from the exact
+// ones in norm for operands of even magnitudes, 4.6e-5 where 1 % of the channels are 50 times
+// larger; of bf16 results, 3 % are the other neighbour of the exact value.
+//
 // The weight tile is the instruction's first operand, so a lane of a result holds columns n
 // of one row m: both scales are one value per lane and block, and four consecutive columns
 // leave in one store.
@@ -15,7 +20,7 @@
 // stages of 128 codes; a stage's weights are replaced once every wavefront has them in
 // registers, its activations at the step's end.  Scales come in chunks of 8 blocks: fetched one
 // block at a time, each instruction touched 64 lines and they were a third of all L1 requests.
-// 4096 x 15360 x 5120: 331 us (1.95 PFLOP/s; 8192^3 at 2.2), where the library's product with one
+// 4096 x 15360 x 5120: 321 us (2.0 PFLOP/s; 8192^3 at 2.2; 357 with f32 results), where the library's product with one
 // scale per tensor reaches 2.9 PFLOP/s at 8192^3; about 8 us of the 82 of a tile are its first
 // loads and its output.  Bound by LDS: a step (2048 cycles of matrix
 // instructions per SIMD) reads 192 KB of fragments and writes 64 KB, and each 1 KB read costs
@@ -26,11 +31,11 @@
 //
 // Streaming kernel (block_gemm_stream_kernel), few rows: bound by reading W.  1 x 11008 x 4096
 // 11.1 us (4.1 TB/s with the launch), 1 x 15360 x 5120 14.2 us (5.5 TB/s), the 64 experts of 8
-// tokens (881 MB) 124-138 us (6.4-7 TB/s).
+// tokens (881 MB) 122-138 us (6.4-7.2 TB/s).
 //
 // Experts: the list of slots (sorted by expert) is cut into m-tiles expert by expert, a
 // workgroup finds its own from the offsets, and rows are gathered by the loads themselves.
-// 4096 tokens x 8 of 64 experts, 4096 x 5120: 855 us (1.6 PFLOP/s): as above, with part of each
+// 4096 tokens x 8 of 64 experts, 4096 x 5120: 838 us (1.6 PFLOP/s): as above, with part of each
 // expert's last tile unused (one that is half empty computes half: 898 -> 875 us) and the weights'
 // 1.3 GB read beside.
 #include <type_traits>

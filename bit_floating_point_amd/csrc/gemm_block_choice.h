@@ -29,9 +29,11 @@ enum class BlockKernel {
 // 4096 x 15360 x 5120 604 / 390 / 356).
 // Experts: lists of the mean length, each with half a tile to spare.  They are bound by reading
 // the experts' weights until the lists are long: streaming up to four rows a list (64 experts of
-// 4096 x 4096, 4 rows: 172 against 182; 8 rows: 214 against 187), then 128 x 128 tiles against
-// 256 x 256 ones, the smaller tiles only where those leave compute units idle (8 rows: 187
-// against 211 with 64 x 64).
+// 4096 x 4096, streamed / tiles: one row 188 / 193, four 187 / 189, eight 191 / 189), then
+// 128 x 128 tiles against 256 x 256 ones, the smaller tiles only where those leave compute units
+// idle (8 rows: 187 against 211 with 64 x 64).  One long list among short ones does not turn the
+// order round, though its weights are streamed once per 16 rows: 256 slots, 128 of them in one
+// list 193 / 211, 192 of them 202 / 209.
 inline BlockKernel block_kernel(int32_t experts, int64_t M, int64_t N) {
     const double lists = experts ? (double)(experts < M ? experts : M) : 1.0, rows = (double)M / lists;
     if (rows <= (experts ? 4 : 16)) {

@@ -9,8 +9,11 @@
 //
 // Measured (us, bytes of inputs and outputs over time): norm of 4096 x 5120 with eight
 // weighted bf16 terms, residual, codes per 128 and bf16 rows 87 (5.5 TB/s); with one term and no
-// rows 35 (4.2); 777 x 11016 f32 with a static scale 30 (3.7); one row of 5120 3.6 in the kernel, 8
-// with the call.  SwiGLU 4096 x 13824 48 (5.9 TB/s).  A copy on this card reaches 4.8 TB/s, reads 6.
+// rows 34 (4.3); 777 x 11016 f32 with a static scale 30.5 (3.6); one row of 5120 3.7 in the kernel, 8
+// with the call; 2^18 rows of 512, one wavefront each, 153 (6.2), but 2^20 rows of 128, which fill
+// 16 of its lanes, 386 (1.0).  SwiGLU 4096 x 13824 47 (6.1 TB/s), with row scales 54 (5.3).  Block
+// weights 15360 x 5120 bf16 50 (4.8), f32 74 (5.3); 32 of 4096 x 5120 bf16 377 (5.3).  A copy on
+// this card reaches 4.8 TB/s, reads 6.
 #include <type_traits>
 
 #include "fp4_device.h"

@@ -11,11 +11,11 @@
 // before its own.  The order does not depend on timing.  Few tokens: one workgroup does all.
 //
 // Bound by the vector instructions of the selection: 16384 tokens of 256 experts in 8 groups
-// 26.8 us, about 18 of them the choice, which issues 476 vector instructions a token, 76 % of
-// its cycles on every SIMD (a round of the top_k is about 20: six fused maxima across the lanes,
+// 26.3 us, 19 of them the choice, which issues 476 vector instructions a token, 76 % of the
+// cycles of every SIMD (a round of the top_k is about 20: six fused maxima across the lanes,
 // the winner's lane by a ballot, the lists' shift by bitwise selects; float maxima, which
 // canonicalize, and array selects took 4 us more).  The placement's 8 us are launch, the table
-// of counts and the order inside each workgroup.  One token of 64 experts: 4.5 us, 6.2 with the
+// of counts and the order inside each workgroup.  One token of 64 experts: 4.2 us, 6.5 with the
 // call.
 #include "fp4_device.h"
 #include "layer_internal.h"

@@ -291,7 +291,8 @@ def fp4_gemm_experts(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
                      y_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None) -> torch.Tensor:
     """Y[s] = X[s // slots_per_row] W[e]^T for the slots s that fp4_route's layout gives to
     expert e: a [rows, K] codes, w [experts, N, K] codes, scales as fp4_gemm_block.  Rows of
-    y whose slot has no expert are not written (without y given, they hold zeros)."""
+    y whose slot has no expert are not written (without y given, they hold zeros: all of it is
+    cleared first, which takes 34 us for the 268 MB of 32768 x 4096 bf16)."""
     _need(a.dim() == 2 and w.dim() == 3, "a must be [rows, K], w [experts, N, K]")
     _need(slots_per_row >= 1 and slots.dim() == 1, "slots must be one list, slots_per_row positive")
     S, (E, N, K), dev = slots.shape[0], w.shape, a.device

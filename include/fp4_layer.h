@@ -15,6 +15,7 @@
  *     16-byte aligned, leading dimensions are multiples of 16 bytes (codes: of 8 bytes),
  *     and the number of columns is a multiple of 8.
  *   - Outputs may not overlap inputs, except where a call says so.
+ *   - Work whose threads would pass 2^32, the most one launch takes, is split over launches.
  */
 #ifndef FP4_LAYER_H_
 #define FP4_LAYER_H_
@@ -173,7 +174,9 @@ size_t fp4_route_workspace_size(int64_t tokens, int32_t experts, int32_t top_k);
  *     which has the scores' order and neither rounds nor underflows -- best first, ties to
  *     the lower index; a token with fewer stays short: expert -1 with weight 0
  *   weights_out[t] = the scores (without bias) of those, divided by their sum with
- *     `renormalise` (a sum of 0 leaves 0), times `scale`
+ *     `renormalise` (a sum of 0 leaves 0), times `scale`; the exponential and the reciprocal
+ *     are the hardware's: a weight is within (2 d + 40) 2^-24 of its exact value, relative, d the
+ *     largest distance of the token's usable logits from their largest (softmax) or from 0
  * Layout (offsets and slots given): slot t * top_k + j belongs to experts_out[t, j];
  * slots holds all slot numbers ordered by expert and, within an expert, ascending, expert
  * e's at offsets[e] .. offsets[e + 1]; the slots of expert -1 follow offsets[experts].
