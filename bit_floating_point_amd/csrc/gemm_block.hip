@@ -136,6 +136,11 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t ntiles) {
     return b < full ? (b % 8) * (full / 8) + b / 8 : b;
 }
 
+// Offsets of any value are safe: ranges that overlap may hold more tiles than 32 bits count, so
+// sums stop at 2^29.  Every tile that a workgroup may take lies below that, and so do the sums
+// before it, which place it.
+__device__ __forceinline__ int tile_sum(int a, int b) { return min(a + b, 1 << 29); }
+
 template <int BM>
 __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n) {
     const int lane = threadIdx.x & 63;
@@ -151,8 +156,8 @@ __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n
     for (int e0 = 0; e0 < p.experts; e0 += 64) {
         int lo, hi, c = range(e0 + lane, lo, hi);
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) c += __shfl_xor(c, o, 64);
-        total += c;
+        for (int o = 1; o < 64; o <<= 1) c = tile_sum(c, __shfl_xor(c, o, 64));
+        total = tile_sum(total, c);
     }
     total = __builtin_amdgcn_readfirstlane(total);
     Tile t{};
@@ -168,12 +173,12 @@ __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int u = __shfl_up(s, o, 64);
-            if (lane >= o) s += u;
+            if (lane >= o) s = tile_sum(s, u);
         }
         const uint64_t hit = __ballot(before + s > want);
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
-            const int first = before + __shfl(s - c, l, 64), mt = __shfl(c, l, 64);
+            const int first = before + (l > 0 ? __shfl(s, l - 1, 64) : 0), mt = __shfl(c, l, 64);
             const int r = __builtin_amdgcn_readfirstlane((int)(at - (int64_t)first * grid_n));
             const int m = __builtin_amdgcn_readfirstlane(mt), from = __builtin_amdgcn_readfirstlane(__shfl(lo, l, 64));
             t.e = __builtin_amdgcn_readfirstlane(e0 + l);
@@ -184,7 +189,7 @@ __device__ __forceinline__ Tile expert_tile(const BlockGemmParams& p, int grid_n
             t.live = true;
             return t;
         }
-        before += __shfl(s, 63, 64);
+        before = tile_sum(before, __shfl(s, 63, 64));
     }
     return t;
 }
