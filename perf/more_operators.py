@@ -335,9 +335,12 @@ def _framework():
 
 
 def _call(st):
+    """The package, and the handle of the cache that a program makes once."""
     F, grids, grans = _framework()
-    case = st["case"]
-    return F, F.KVCache(st["k_cache"], st["v_cache"], st["k_scales"], st["v_scales"], grids[case["store"]], grans[case["scales"]])
+    if "cache" not in st:
+        case = st["case"]
+        st["cache"] = F.KVCache(st["k_cache"], st["v_cache"], st["k_scales"], st["v_scales"], grids[case["store"]], grans[case["scales"]])
+    return F, st["cache"]
 
 
 def _call_write(st):
