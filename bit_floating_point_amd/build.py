@@ -17,7 +17,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["quant.hip", "gemm_w4a16.hip", "gemm_w4a4.hip", "gemm_lut.hip", "gemm_f8f6.hip", "search.hip", "norm_quant.hip",
-           "gemm_block.hip", "route.hip", "fp4_api.cpp", "layer_api.cpp"]
+           "gemm_block.hip", "route.hip", "cache.hip", "attend.hip", "attend_bf16.hip", "attend_e4m3.hip", "attend_e5m2.hip",
+           "attend_e2m1.hip", "fp4_api.cpp", "layer_api.cpp", "cache_api.cpp"]
 
 # -ffp-contract=off: no silent a*b+c fusion, so every rounding is the one written
 # (fused multiply-adds are explicit); packed-fp32 instructions are disabled.

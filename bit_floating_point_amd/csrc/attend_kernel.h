@@ -1,0 +1,474 @@
+// Attention of one new token per sequence over the pages of a cache: the kernel over a part
+// of a sequence.  Instances: attend_bf16.hip, attend_e4m3.hip, attend_e5m2.hip, attend_e2m1.hip.
+//
+// Mathematics.  One pass: m the largest z seen so far (any upper estimate to 2^8 will do), l = sum of
+// 2^(z - m), O = sum of 2^(z - m) V; a larger z scales l and O by 2^(m - m').  Parts (m, l, O)
+// are joined with factors 2^(m_i - M).  z is in powers of two: the scale holds log2 e.
+//
+// Layout.  A wavefront takes 32 positions at a time, as two halves of 16 (a page holds a multiple of 16
+// positions, so a half lies in one page and has a base address of its own), with the 16x16x32
+// bf16 matrix instruction, whose operands a lane holds as 8 values along the summed dimension:
+//   Z^T = K Q^T: rows are 16 positions, columns 16 query heads, summed over 32 columns of K;
+//   O^T = V^T P^T: rows are 16 columns of V, columns the heads, summed over the 32 positions.
+// Lane (n = lane % 16, g = lane / 16) gets Z of head n and positions 4g .. 4g + 3 of both halves; the
+// positions' order along the sum over P is free, so those 8 numbers ARE the lane's operand
+// of the second product.  Maxima, sums and factors of head n stay in its lanes.
+//   K: lane (n, g) reads row n, g's pieces of it, as they are needed (the order of columns along
+//      the sum is free too: q is read in the same order).
+//   V: lane (n, g) reads the same few columns of its 8 positions, 16 lanes a whole row; pairs of positions
+//      are interleaved by byte permutes and converted two at a time.
+// Codes convert to bf16 exactly, scales of rows go into z and into the weights p = 2^(z - m).
+#pragma once
+#include <type_traits>
+
+#include "cache_internal.h"
+#include "unit_codes.h"
+
+namespace fp4 {
+
+namespace attend {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = kAttendWaves * 64;
+constexpr float kNothing = -3.0e38f;  // the maximum where no position was seen
+constexpr float kSlack = 8.0f;        // z may pass m by this: weights to 2^8
+
+// `total` things in pieces of powers of two, none above `most`: number, start and size
+constexpr int piece_size(int total, int most, int l) {
+    int at = 0, size = 0;
+    for (int i = 0; i <= l; i++) {
+        at += size;
+        size = 1;
+        while (2 * size <= most && 2 * size <= total - at) size *= 2;
+    }
+    return size;
+}
+constexpr int piece_first(int total, int most, int l) {
+    int at = 0;
+    for (int i = 0; i < l; i++) at += piece_size(total, most, i);
+    return at;
+}
+constexpr int pieces(int total, int most) {
+    int n = 0;
+    while (piece_first(total, most, n) < total) n++;
+    return n;
+}
+
+// What a lane loads of a tile.  K: D / 32 steps of 8 columns a lane, in loads of up to 16 bytes.
+// V: D / 16 columns a lane, likewise.
+template <int STORE, int D>
+struct Plan {
+    static constexpr int kBits = STORE == kStoreBf16 ? 16 : STORE == kStoreE2m1 ? 4 : 8;
+    static constexpr int kSteps = D / 32, kStepBytes = kBits;  // bytes of 8 columns
+    static constexpr int kLoads = pieces(kSteps, 16 / kStepBytes);
+    static constexpr int k_first(int l) { return piece_first(kSteps, 16 / kStepBytes, l); }
+    static constexpr int k_steps(int l) { return piece_size(kSteps, 16 / kStepBytes, l); }
+    static constexpr int kCols = D / 16;
+    static constexpr int vLoads = pieces(kCols, 128 / kBits);
+    static constexpr int v_first(int l) { return piece_first(kCols, 128 / kBits, l); }
+    static constexpr int v_cols(int l) { return piece_size(kCols, 128 / kBits, l); }
+    static constexpr int v_bytes(int l) { return v_cols(l) * kBits / 8; }
+    static constexpr int v_words(int l) { return (v_bytes(l) + 3) / 4; }
+    static constexpr int v_word_first(int l) { return l == 0 ? 0 : v_word_first(l - 1) + v_words(l - 1); }
+    static constexpr int kWords = kSteps * kStepBytes / 4, vWords = v_word_first(vLoads);
+};
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const uint8_t* base, uint32_t off, uint32_t* w) {
+    const uint8_t* a = base + off;
+    if constexpr (BYTES == 16) {
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a));
+        w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+    } else if constexpr (BYTES == 8) {
+        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a));
+        w[0] = v[0], w[1] = v[1];
+    } else if constexpr (BYTES == 4) {
+        w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a));
+    } else if constexpr (BYTES == 2) {
+        w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(a));
+    } else {
+        w[0] = __builtin_nontemporal_load(a);
+    }
+}
+
+__device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ bf16x8 operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
+}
+
+// two codes of a word as bf16: those in half `HALF` (8 bits) or byte `AT` (4 bits)
+template <int STORE, int AT>
+__device__ __forceinline__ uint32_t two_values(uint32_t w) {
+    if constexpr (STORE == kStoreE4m3) return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, AT != 0));
+    else if constexpr (STORE == kStoreE5m2) return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, AT != 0));
+    else return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, AT));
+}
+
+// 8 columns of a row of K, from the words at w
+template <int STORE>
+__device__ __forceinline__ bf16x8 key_operand(const uint32_t* w) {
+    if constexpr (STORE == kStoreBf16) {
+        return operand(w[0], w[1], w[2], w[3]);
+    } else if constexpr (STORE == kStoreE2m1) {
+        return operand(two_values<STORE, 0>(w[0]), two_values<STORE, 1>(w[0]), two_values<STORE, 2>(w[0]), two_values<STORE, 3>(w[0]));
+    } else {
+        return operand(two_values<STORE, 0>(w[0]), two_values<STORE, 1>(w[0]), two_values<STORE, 0>(w[1]), two_values<STORE, 1>(w[1]));
+    }
+}
+
+// Column E of the word w[.] of 8 positions: pairs of positions side by side.  The interleaved
+// words serve 2 (bf16), 4 (8 bits) or 8 (4 bits) columns; the compiler keeps them.
+template <int STORE, int E>
+__device__ __forceinline__ uint32_t value_pair(uint32_t a, uint32_t b) {
+    if constexpr (STORE == kStoreBf16) {
+        return __builtin_amdgcn_perm(b, a, E == 0 ? 0x05040100u : 0x07060302u);
+    } else if constexpr (STORE == kStoreE2m1) {
+        constexpr uint32_t low = 0x0f0f0f0fu;
+        const uint32_t w = E % 2 == 0 ? (a & low) | ((b << 4) & ~low) : ((a >> 4) & low) | (b & ~low);
+        return two_values<STORE, E / 2>(w);
+    } else {
+        return two_values<STORE, E % 2>(__builtin_amdgcn_perm(b, a, E < 2 ? 0x05010400u : 0x07030602u));
+    }
+}
+
+__device__ __forceinline__ float low_half(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_half(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// x (8 values) as sums of N bf16 terms, each the nearest to what is left
+template <int N>
+__device__ __forceinline__ void terms_of(float x[8], bf16x8 out[N]) {
+#pragma unroll
+    for (int t = 0; t < N; t++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+            x[2 * i] -= low_half(w[i]);
+            x[2 * i + 1] -= high_half(w[i]);
+        }
+        out[t] = operand(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__device__ __forceinline__ float power2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// f(integral_constant<0>) .. f(integral_constant<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void repeat(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        repeat<N, I + 1>(f);
+    }
+}
+
+// four consecutive scales of a half's rows
+template <typename T>
+__device__ __forceinline__ void scales4(const CacheParams& c, const void* scales, int64_t at, float out[4]) {
+    if (c.scales == kScaleRowF32) {
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(scales) + at);
+        out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const __half*>(scales) + at);
+        const float2 a = __half22float2(__builtin_bit_cast(__half2, v.x)), b = __half22float2(__builtin_bit_cast(__half2, v.y));
+        out[0] = a.x, out[1] = a.y, out[2] = b.x, out[3] = b.y;
+    }
+}
+
+// WIDE: q or y is f32, and its terms three.
+template <int STORE, int D, bool WIDE>
+__global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_t first_sequence) {
+    using L = Plan<STORE, D>;
+    constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
+    constexpr int kRound = 8;  // heads whose parts are joined at a time
+    __shared__ float joined[kAttendWaves][kRound][D + 4];
+    __shared__ float stats[kAttendWaves][kHeadTile][2];
+
+    const CacheParams& c = p.c;
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // workgroup -> sequence, kv head, tile of its query heads, part
+    const uint32_t tiles = (uint32_t)(p.share + kHeadTile - 1) / kHeadTile;
+    uint32_t at = blockIdx.x;
+    const int split = (int)(at % (uint32_t)p.splits);
+    at /= (uint32_t)p.splits;
+    const int head_tile = (int)(at % tiles);
+    at /= tiles;
+    const int kv_head = (int)(at % (uint32_t)c.kv_heads);
+    const int64_t sequence = first_sequence + at / (uint32_t)c.kv_heads;
+    const int heads = min(p.share - head_tile * kHeadTile, kHeadTile);  // of this tile
+    const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeadTile;
+
+    const int32_t length = max(0, min(p.lengths[sequence], p.capacity));
+    const SplitRange range = split_range(length, p.window, p.splits);
+    if (split > 0 && split >= range.used) return;
+    const int begin = range.first + split * range.chunk;
+    const int end = length - begin < range.chunk ? length : begin + range.chunk;
+    const int all = (end - begin + kTilePositions - 1) / kTilePositions;  // tiles of the part
+    const int count = (all - wave + kAttendWaves - 1) / kAttendWaves;     // of this wavefront (at most 0: none)
+
+    // q of head n, in K's order of columns
+    bf16x8 q[kQTerms][L::kSteps];
+    {
+        const bool there = n < heads;
+        const int64_t row = sequence * p.ldq + (first_head + n) * D;
+        repeat<L::kLoads>([&](auto l) {
+            constexpr int first = L::k_first(l), steps = L::k_steps(l);
+#pragma unroll
+            for (int i = 0; i < steps; i++) {
+                float x[8] = {};
+                if (there) get8(p.q, p.q_bf16, row + first * 32 + g * 8 * steps + 8 * i, x);
+                bf16x8 t[kQTerms];
+                terms_of<kQTerms>(x, t);
+#pragma unroll
+                for (int k = 0; k < kQTerms; k++) q[k][first + i] = t[k];
+            }
+        });
+    }
+
+    float m = kNothing, l = 0.0f;
+    f32x4 acc[L::kCols];
+#pragma unroll
+    for (int j = 0; j < L::kCols; j++) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    uint32_t kw[2][L::kWords], vw[8][L::vWords];
+    float ks[8], vs[8];
+    const bool row_scales = c.scales >= kScaleRowF32;
+    float k_all = p.scale_log2, v_all = 1.0f;
+    if (c.scales == kScaleGiven) {
+        k_all *= *reinterpret_cast<const float*>(c.k_scales);
+        v_all = *reinterpret_cast<const float*>(c.v_scales);
+    }
+
+    // The pages of 32 of this wavefront's tiles, one half of a tile a lane; -1: not there.
+    const int32_t* table = p.table + sequence * p.ld_table;
+    int page_ids = -1;
+    auto find_pages = [&](int i) {
+        const int t = begin + ((i + (lane >> 1)) * kAttendWaves + wave) * kTilePositions + 16 * (lane & 1);
+        page_ids = t < end ? page_at(table + (t >> c.page_log), c.pages) : -1;
+    };
+    // a tile of this wavefront: its first position and its halves' pages (-1: nothing there to
+    // be seen; page 0 is read in its place and not used)
+    struct Tile {
+        int t, page[2];
+    };
+    auto tile_of = [&](int i) {
+        Tile r;
+        r.t = begin + (i * kAttendWaves + wave) * kTilePositions;
+        r.page[0] = __builtin_amdgcn_readlane(page_ids, 2 * (i & 31));
+        r.page[1] = __builtin_amdgcn_readlane(page_ids, 2 * (i & 31) + 1);
+        return r;
+    };
+    const int slots = (1 << c.page_log) - 1;
+    auto half_base = [&](const Tile& tile, int h) {
+        return max(tile.page[h], 0) * c.stride_page + kv_head * c.stride_head + (int64_t)((tile.t + 16 * h) & slots) * c.stride_row;
+    };
+    auto load_scales = [&](const Tile& tile, const void* scales, float out[8]) {
+        if (row_scales) {
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                scales4<float>(c, scales, (((int64_t)max(tile.page[h], 0) * c.kv_heads + kv_head) << c.page_log) + ((tile.t + 16 * h) & slots) + 4 * g,
+                               out + 4 * h);
+        }
+    };
+    auto load_keys = [&](const Tile& tile) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint8_t* base = c.k + half_base(tile, h);
+            repeat<L::kLoads>([&](auto x) {
+                constexpr int first = L::k_first(x), steps = L::k_steps(x), bytes = steps * L::kStepBytes;
+                load_bytes<bytes>(base, (uint32_t)n * c.stride_row + (uint32_t)(first * 4 * L::kStepBytes + g * bytes), kw[h] + first * L::kStepBytes / 4);
+            });
+        }
+        load_scales(tile, c.k_scales, ks);
+    };
+    auto load_values = [&](const Tile& tile) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const uint8_t* base = c.v + half_base(tile, j / 4) + (int64_t)(j % 4) * c.stride_row;
+            repeat<L::vLoads>([&](auto x) {
+                constexpr int bytes = L::v_bytes(x);
+                load_bytes<bytes>(base, (uint32_t)(4 * g) * c.stride_row + (uint32_t)(L::v_first(x) * 2 * L::kBits + n * bytes), vw[j] + L::v_word_first(x));
+            });
+        }
+        load_scales(tile, c.v_scales, vs);
+    };
+
+    Tile tile{};
+    if (count > 0) {
+        find_pages(0);
+        tile = tile_of(0);
+        load_keys(tile);
+        load_values(tile);
+    }
+    for (int i = 0; i < count; i++) {
+        // Z^T of both halves
+        f32x4 z2[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            z2[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < L::kSteps; s++) {
+                const bf16x8 a = key_operand<STORE>(kw[h] + s * L::kStepBytes / 4);
+#pragma unroll
+                for (int k = kQTerms - 1; k >= 0; k--) z2[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z2[h], 0, 0, 0);
+            }
+        }
+        float z[8], sv[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) z[j] = z2[j / 4][j % 4] * (row_scales ? ks[j] * k_all : k_all);
+        // the next tile's keys are on their way from here on
+        Tile next{};
+        if (i + 1 < count) {
+            if (((i + 1) & 31) == 0) find_pages(i + 1);
+            next = tile_of(i + 1);
+            load_keys(next);
+        }
+        // what is not seen: no weight, whatever its rows and scales hold
+        bool seen[8];
+        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && tile.page[0] >= 0 && tile.page[1] >= 0;
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
+                seen[j] = t >= range.begin && t < end && tile.page[j / 4] >= 0;
+                z[j] = seen[j] ? z[j] : kNothing;
+            }
+        }
+        float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float to = fmaxf(m, top), f = power2(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int j = 0; j < L::kCols; j++) acc[j] *= f;
+        }
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            w[j] = power2(z[j] - m);
+            sv[j] = row_scales ? vs[j] : 1.0f;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                w[j] = seen[j] ? w[j] : 0.0f;
+                sv[j] = seen[j] ? sv[j] : 0.0f;
+#pragma unroll
+                for (int u = 0; u < L::vWords; u++) vw[j][u] = seen[j] ? vw[j][u] : 0u;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            l += w[j];
+            w[j] *= sv[j];
+        }
+        bf16x8 weight[kPTerms];
+        terms_of<kPTerms>(w, weight);
+        // O^T: a column of V at a time
+        repeat<L::vLoads>([&](auto x) {
+            repeat<L::v_cols(x)>([&](auto e) {
+                constexpr int per = 32 / L::kBits, word = L::v_word_first(x) + e / per;
+                const bf16x8 a = operand(value_pair<STORE, e % per>(vw[0][word], vw[1][word]), value_pair<STORE, e % per>(vw[2][word], vw[3][word]),
+                                         value_pair<STORE, e % per>(vw[4][word], vw[5][word]), value_pair<STORE, e % per>(vw[6][word], vw[7][word]));
+                f32x4& o = acc[L::v_first(x) + e];
+#pragma unroll
+                for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[k], o, 0, 0, 0);
+            });
+        });
+        if (i + 1 < count) load_values(next);
+        tile = next;
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+
+    // the wavefronts' parts, joined; lane (n, g) holds columns first * 16 + cols (4 g + i) + e
+    if (g == 0) {
+        stats[wave][n][0] = m;
+        stats[wave][n][1] = l;
+    }
+    const int64_t unit = sequence * p.heads + first_head;
+    for (int r = 0; r < heads; r += kRound) {
+        if (r > 0) __syncthreads();
+        if (n >= r && n < r + kRound) {
+            repeat<L::vLoads>([&](auto x) {
+                repeat<L::v_cols(x)>([&](auto e) {
+                    constexpr int cols = L::v_cols(x), first = L::v_first(x);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) joined[wave][n - r][first * 16 + cols * (4 * g + i) + e] = acc[first + e][i];
+                });
+            });
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < min(heads - r, kRound) * D; e += kThreads) {
+            const int row = e / D, col = e % D;
+            float top = stats[0][r + row][0];
+#pragma unroll
+            for (int v = 1; v < kAttendWaves; v++) top = fmaxf(top, stats[v][r + row][0]);
+            float sum = 0.0f, o = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kAttendWaves; v++) {
+                const float f = power2(stats[v][r + row][0] - top);
+                sum = __builtin_fmaf(stats[v][r + row][1], f, sum);
+                o = __builtin_fmaf(joined[v][row][col], f, o);
+            }
+            o *= v_all;
+            const int64_t head = unit + r + row;
+            if (range.used > 1) {
+                p.part_o[(head * p.splits + split) * D + col] = o;
+                if (col == 0) {
+                    p.part_ml[(head * p.splits + split) * 2] = top;
+                    p.part_ml[(head * p.splits + split) * 2 + 1] = sum;
+                }
+            } else {
+                const float y = sum > 0.0f ? o / sum : sum == 0.0f ? 0.0f : sum;
+                const int64_t to = sequence * p.ldy + (first_head + r + row) * D + col;
+                if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[to] = (__bf16)y;
+                else reinterpret_cast<float*>(p.y)[to] = y;
+                if (p.lse && col == 0) p.lse[head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0x1.62e43p-1f;
+            }
+        }
+    }
+}
+
+// the kernel for a head dimension and width of one kind of cache
+template <int STORE>
+hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
+    const bool wide = !p.q_bf16 || !p.y_bf16;
+    const int64_t tiles = (p.share + kHeadTile - 1) / kHeadTile, each = (int64_t)p.c.kv_heads * tiles * p.splits;
+    const int64_t most = max_workgroups(kThreads) / each;
+    for (int64_t first = 0; first < p.sequences; first += most) {
+        const int64_t n = p.sequences - first < most ? p.sequences - first : most;
+        const dim3 grid((unsigned)(n * each));
+        auto go = [&](auto dim) {
+            constexpr int D = decltype(dim)::value;
+            if (wide) attend_kernel<STORE, D, true><<<grid, kThreads, 0, s>>>(p, first);
+            else attend_kernel<STORE, D, false><<<grid, kThreads, 0, s>>>(p, first);
+        };
+        switch (p.c.head_dim) {
+            case 64: go(std::integral_constant<int, 64>{}); break;
+            case 96: go(std::integral_constant<int, 96>{}); break;
+            case 128: go(std::integral_constant<int, 128>{}); break;
+            case 192: go(std::integral_constant<int, 192>{}); break;
+            default: go(std::integral_constant<int, 256>{}); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace attend
+
+hipError_t launch_attend_bf16(const AttendParams& p, hipStream_t s);
+hipError_t launch_attend_e4m3(const AttendParams& p, hipStream_t s);
+hipError_t launch_attend_e5m2(const AttendParams& p, hipStream_t s);
+hipError_t launch_attend_e2m1(const AttendParams& p, hipStream_t s);
+
+}  // namespace fp4
