@@ -78,22 +78,28 @@ struct Plan {
     static constexpr int kWords = kSteps * kStepBytes / 4, vWords = v_word_first(vLoads);
 };
 
+// BYTES of a lane at byte `off` + `more` (one of all lanes) past a buffer's start.  Buffer loads: base
+// and `more` are scalars, so a load costs no vector instruction for its address.
+constexpr int kOnce = 2;  // nontemporal
 template <int BYTES>
-__device__ __forceinline__ void load_bytes(const uint8_t* base, uint32_t off, uint32_t* w) {
-    const uint8_t* a = base + off;
+__device__ __forceinline__ void load_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t more, uint32_t* w) {
     if constexpr (BYTES == 16) {
-        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a));
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, more, kOnce);
         w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
     } else if constexpr (BYTES == 8) {
-        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a));
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, more, kOnce);
         w[0] = v[0], w[1] = v[1];
     } else if constexpr (BYTES == 4) {
-        w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a));
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, more, kOnce);
     } else if constexpr (BYTES == 2) {
-        w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(a));
+        w[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, more, kOnce);
     } else {
-        w[0] = __builtin_nontemporal_load(a);
+        w[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, more, kOnce);
     }
+}
+// the buffer from `base` on: pages and scales are addressed by their own starts, offsets stay below 2^31
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t off) {
+    return buf_make(reinterpret_cast<const uint8_t*>(base) + off, 0x7fffffff);
 }
 
 __device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
@@ -166,21 +172,27 @@ __device__ __forceinline__ void repeat(F&& f) {
     }
 }
 
-// four consecutive scales of a half's rows
-template <typename T>
-__device__ __forceinline__ void scales4(const CacheParams& c, const void* scales, int64_t at, float out[4]) {
-    if (c.scales == kScaleRowF32) {
-        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(scales) + at);
-        out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const __half*>(scales) + at);
-        const float2 a = __half22float2(__builtin_bit_cast(__half2, v.x)), b = __half22float2(__builtin_bit_cast(__half2, v.y));
-        out[0] = a.x, out[1] = a.y, out[2] = b.x, out[3] = b.y;
+// Row scales of a tile: a lane's four of each half, as they are stored until they are used.
+// SCALES: kScaleRowF32, kScaleRowF16, or kScaleNone where there are none (one given scale is the
+// caller's factor).
+template <int SCALES>
+struct RowScales {
+    static constexpr int kBytes = SCALES == kScaleRowF32 ? 4 : SCALES == kScaleRowF16 ? 2 : 0;
+    uint32_t w[2][4];
+    // `first`: index of the half's first scale
+    __device__ __forceinline__ void load(const void* scales, int64_t first, int half, int g) {
+        if constexpr (kBytes) load_bytes<4 * kBytes>(buffer_at(scales, first * kBytes), (uint32_t)(4 * g * kBytes), 0, w[half]);
     }
-}
+    __device__ __forceinline__ float get(int j) const {
+        const uint32_t* h = w[j / 4];
+        if constexpr (SCALES == kScaleRowF32) return __uint_as_float(h[j % 4]);
+        else if constexpr (SCALES == kScaleRowF16) return __half2float(__ushort_as_half((uint16_t)(h[j % 4 / 2] >> (16 * (j % 2)))));
+        else return 1.0f;
+    }
+};
 
 // WIDE: q or y is f32, and its terms three.
-template <int STORE, int D, bool WIDE>
+template <int STORE, int SCALES, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_t first_sequence) {
     using L = Plan<STORE, D>;
     constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
     const int heads = min(p.share - head_tile * kHeadTile, kHeadTile);  // of this tile
     const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeadTile;
 
-    const int32_t length = max(0, min(p.lengths[sequence], p.capacity));
+    const int32_t length = __builtin_amdgcn_readfirstlane(max(0, min(p.lengths[sequence], p.capacity)));
     const SplitRange range = split_range(length, p.window, p.splits);
     if (split > 0 && split >= range.used) return;
     const int begin = range.first + split * range.chunk;
@@ -236,8 +248,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
     for (int j = 0; j < L::kCols; j++) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     uint32_t kw[2][L::kWords], vw[8][L::vWords];
-    float ks[8], vs[8];
-    const bool row_scales = c.scales >= kScaleRowF32;
+    constexpr bool kRows = SCALES != kScaleNone;
+    RowScales<SCALES> ks, vs;
     float k_all = p.scale_log2, v_all = 1.0f;
     if (c.scales == kScaleGiven) {
         k_all *= *reinterpret_cast<const float*>(c.k_scales);
@@ -267,35 +279,34 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
     auto half_base = [&](const Tile& tile, int h) {
         return max(tile.page[h], 0) * c.stride_page + kv_head * c.stride_head + (int64_t)((tile.t + 16 * h) & slots) * c.stride_row;
     };
-    auto load_scales = [&](const Tile& tile, const void* scales, float out[8]) {
-        if (row_scales) {
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-                scales4<float>(c, scales, (((int64_t)max(tile.page[h], 0) * c.kv_heads + kv_head) << c.page_log) + ((tile.t + 16 * h) & slots) + 4 * g,
-                               out + 4 * h);
-        }
+    auto half_scales = [&](const Tile& tile, int h) {
+        return (((int64_t)max(tile.page[h], 0) * c.kv_heads + kv_head) << c.page_log) + ((tile.t + 16 * h) & slots);
     };
+    const uint32_t key_row = (uint32_t)n * c.stride_row, value_row = (uint32_t)(4 * g) * c.stride_row;
     auto load_keys = [&](const Tile& tile) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const uint8_t* base = c.k + half_base(tile, h);
+            const auto rows = buffer_at(c.k, half_base(tile, h));
             repeat<L::kLoads>([&](auto x) {
                 constexpr int first = L::k_first(x), steps = L::k_steps(x), bytes = steps * L::kStepBytes;
-                load_bytes<bytes>(base, (uint32_t)n * c.stride_row + (uint32_t)(first * 4 * L::kStepBytes + g * bytes), kw[h] + first * L::kStepBytes / 4);
+                load_bytes<bytes>(rows, key_row + (uint32_t)(first * 4 * L::kStepBytes + g * bytes), 0, kw[h] + first * L::kStepBytes / 4);
             });
+            ks.load(c.k_scales, half_scales(tile, h), h, g);
         }
-        load_scales(tile, c.k_scales, ks);
     };
     auto load_values = [&](const Tile& tile) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const uint8_t* base = c.v + half_base(tile, j / 4) + (int64_t)(j % 4) * c.stride_row;
-            repeat<L::vLoads>([&](auto x) {
-                constexpr int bytes = L::v_bytes(x);
-                load_bytes<bytes>(base, (uint32_t)(4 * g) * c.stride_row + (uint32_t)(L::v_first(x) * 2 * L::kBits + n * bytes), vw[j] + L::v_word_first(x));
-            });
+        for (int h = 0; h < 2; h++) {
+            const auto rows = buffer_at(c.v, half_base(tile, h));
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                repeat<L::vLoads>([&](auto x) {
+                    constexpr int bytes = L::v_bytes(x);
+                    load_bytes<bytes>(rows, value_row + (uint32_t)(L::v_first(x) * 2 * L::kBits + n * bytes), (uint32_t)j * c.stride_row,
+                                      vw[4 * h + j] + L::v_word_first(x));
+                });
+            vs.load(c.v_scales, half_scales(tile, h), h, g);
         }
-        load_scales(tile, c.v_scales, vs);
     };
 
     Tile tile{};
@@ -305,7 +316,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
         load_keys(tile);
         load_values(tile);
     }
-    for (int i = 0; i < count; i++) {
+    // Tile i; with `more`, the loads of tile i + 1 start where the registers of i's keys and then of its
+    // values are free.  (The last tile is a copy of its own: a load under a condition would be
+    // waited for where the condition ends.)
+    auto step = [&](int i, auto more) {
         // Z^T of both halves
         f32x4 z2[2];
 #pragma unroll
@@ -318,12 +332,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
                 for (int k = kQTerms - 1; k >= 0; k--) z2[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z2[h], 0, 0, 0);
             }
         }
-        float z[8], sv[8];
+        float z[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) z[j] = z2[j / 4][j % 4] * (row_scales ? ks[j] * k_all : k_all);
-        // the next tile's keys are on their way from here on
+        for (int j = 0; j < 8; j++) z[j] = z2[j / 4][j % 4] * (kRows ? ks.get(j) * k_all : k_all);
         Tile next{};
-        if (i + 1 < count) {
+        if constexpr (more) {
             if (((i + 1) & 31) == 0) find_pages(i + 1);
             next = tile_of(i + 1);
             load_keys(next);
@@ -351,23 +364,23 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
         }
         float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            w[j] = power2(z[j] - m);
-            sv[j] = row_scales ? vs[j] : 1.0f;
-        }
+        for (int j = 0; j < 8; j++) w[j] = power2(z[j] - m);
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                w[j] = seen[j] ? w[j] : 0.0f;
-                sv[j] = seen[j] ? sv[j] : 0.0f;
-#pragma unroll
-                for (int u = 0; u < L::vWords; u++) vw[j][u] = seen[j] ? vw[j][u] : 0u;
-            }
+            for (int j = 0; j < 8; j++) w[j] = seen[j] ? w[j] : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             l += w[j];
-            w[j] *= sv[j];
+            if constexpr (kRows) w[j] *= vs.get(j);
+        }
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if constexpr (kRows) w[j] = seen[j] ? w[j] : 0.0f;
+#pragma unroll
+                for (int u = 0; u < L::vWords; u++) vw[j][u] = seen[j] ? vw[j][u] : 0u;
+            }
         }
         bf16x8 weight[kPTerms];
         terms_of<kPTerms>(w, weight);
@@ -382,9 +395,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
                 for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[k], o, 0, 0, 0);
             });
         });
-        if (i + 1 < count) load_values(next);
-        tile = next;
-    }
+        if constexpr (more) {
+            load_values(next);
+            tile = next;
+        }
+    };
+    for (int i = 0; i + 1 < count; i++) step(i, std::true_type{});
+    if (count > 0) step(count - 1, std::false_type{});
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
 
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
     }
 }
 
-// the kernel for a head dimension and width of one kind of cache
+// the kernel for the scales, the head dimension and the types of a call on one kind of cache
 template <int STORE>
 hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
     const bool wide = !p.q_bf16 || !p.y_bf16;
@@ -446,10 +463,17 @@ hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
     for (int64_t first = 0; first < p.sequences; first += most) {
         const int64_t n = p.sequences - first < most ? p.sequences - first : most;
         const dim3 grid((unsigned)(n * each));
+        auto with = [&](auto dim, auto scales) {
+            constexpr int D = decltype(dim)::value, SCALES = decltype(scales)::value;
+            if (wide) attend_kernel<STORE, SCALES, D, true><<<grid, kThreads, 0, s>>>(p, first);
+            else attend_kernel<STORE, SCALES, D, false><<<grid, kThreads, 0, s>>>(p, first);
+        };
         auto go = [&](auto dim) {
-            constexpr int D = decltype(dim)::value;
-            if (wide) attend_kernel<STORE, D, true><<<grid, kThreads, 0, s>>>(p, first);
-            else attend_kernel<STORE, D, false><<<grid, kThreads, 0, s>>>(p, first);
+            if constexpr (STORE != kStoreBf16) {
+                if (p.c.scales == kScaleRowF32) return with(dim, std::integral_constant<int, kScaleRowF32>{});
+                if (p.c.scales == kScaleRowF16) return with(dim, std::integral_constant<int, kScaleRowF16>{});
+            }
+            with(dim, std::integral_constant<int, kScaleNone>{});
         };
         switch (p.c.head_dim) {
             case 64: go(std::integral_constant<int, 64>{}); break;
