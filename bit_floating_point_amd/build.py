@@ -28,8 +28,9 @@ CFLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-ffp-contract
 
 
 # These GEMM kernels count their outstanding loads in their waits; a register spill would
-# add scratch memory operations to those counts, so they must not spill.
-NO_SPILL = ("gemm_w4a4.hip", "gemm_lut.hip", "gemm_block.hip")
+# add scratch memory operations to those counts, so they must not spill.  Nor may the attention
+# over a cache, whose next tile waits in registers.
+NO_SPILL = ("gemm_w4a4.hip", "gemm_lut.hip", "gemm_block.hip", "attend_bf16.hip", "attend_e4m3.hip", "attend_e5m2.hip", "attend_e2m1.hip")
 
 
 def _check_no_spill(src: str, remarks: str) -> None:

@@ -10,6 +10,7 @@ namespace fp4 {
 namespace {
 
 constexpr int kJoinThreads = 256;
+constexpr int kFewParts = 16;
 
 __device__ __forceinline__ float block_reduce(float v, float* part, bool largest) {
 #pragma unroll
@@ -27,15 +28,33 @@ __device__ __forceinline__ float block_reduce(float v, float* part, bool largest
 
 }  // namespace
 
-// D columns as D / 4 lanes of four, the parts dealt to as many groups of lanes as there are
+// one value of the result: column `col` of head `unit`, O over the sum of weights
+__device__ __forceinline__ void put_joined(const AttendParams& p, int64_t unit, int64_t sequence, int dim, int col, float o, float sum) {
+    const float y = sum > 0.0f ? o / sum : sum == 0.0f ? 0.0f : sum;
+    const int64_t to = sequence * p.ldy + (unit - sequence * p.heads) * dim + col;
+    if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[to] = (__bf16)y;
+    else reinterpret_cast<float*>(p.y)[to] = y;
+}
+__device__ __forceinline__ void put_lse(const AttendParams& p, int64_t unit, float top, float sum) {
+    if (p.lse) p.lse[unit] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0x1.62e43p-1f;
+}
+__device__ __forceinline__ SplitRange range_of(const AttendParams& p, int64_t sequence) {
+    return split_range(max(0, min(p.lengths[sequence], p.capacity)), p.window, p.splits);
+}
+__device__ __forceinline__ void add4(float4& a, const float4& v, float w) {
+    a.x = __builtin_fmaf(v.x, w, a.x), a.y = __builtin_fmaf(v.y, w, a.y);
+    a.z = __builtin_fmaf(v.z, w, a.z), a.w = __builtin_fmaf(v.w, w, a.w);
+}
+
+// Many parts: a workgroup per head.  D columns as D / 4 lanes of four, the parts dealt to as many
+// groups of lanes as there are.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams p, int64_t first) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams p, int64_t first, int64_t) {
     constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
     __shared__ float weight[kMostSplits], part[2][kJoinThreads / 64];
     __shared__ float4 sums[kGroups][kLanes];
     const int64_t unit = first + blockIdx.x, sequence = unit / p.heads;
-    const int32_t length = max(0, min(p.lengths[sequence], p.capacity));
-    const SplitRange range = split_range(length, p.window, p.splits);
+    const SplitRange range = range_of(p, sequence);
     if (range.used <= 1) return;
     const float* ml = p.part_ml + unit * p.splits * 2;
     const bool there = (int)threadIdx.x < range.used;
@@ -49,12 +68,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams 
         const float4* o = reinterpret_cast<const float4*>(p.part_o + unit * p.splits * D) + col;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int i = group; i < range.used; i += kGroups) {
-            const float4 v = o[(int64_t)i * kLanes];
-            const float w = weight[i];
-            a.x = __builtin_fmaf(v.x, w, a.x), a.y = __builtin_fmaf(v.y, w, a.y);
-            a.z = __builtin_fmaf(v.z, w, a.z), a.w = __builtin_fmaf(v.w, w, a.w);
-        }
+        for (int i = group; i < range.used; i += kGroups) add4(a, o[(int64_t)i * kLanes], weight[i]);
         sums[group][col] = a;
     }
     __syncthreads();
@@ -62,13 +76,70 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams 
         float o = 0.0f;
 #pragma unroll
         for (int i = 0; i < kGroups; i++) o += reinterpret_cast<const float*>(&sums[i][0])[threadIdx.x];
-        const float y = sum > 0.0f ? o / sum : sum == 0.0f ? 0.0f : sum;
-        const int64_t to = sequence * p.ldy + (unit - sequence * p.heads) * D + threadIdx.x;
-        if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[to] = (__bf16)y;
-        else reinterpret_cast<float*>(p.y)[to] = y;
-        if (p.lse && threadIdx.x == 0) p.lse[unit] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0x1.62e43p-1f;
+        put_joined(p, unit, sequence, D, threadIdx.x, o, sum);
+        if (threadIdx.x == 0) put_lse(p, unit, top, sum);
     }
 }
+
+// Few parts (at most 64): a wavefront per head, no barriers.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_few_kernel(AttendParams p, int64_t first, int64_t units) {
+    constexpr int kLanes = D / 4, kGroups = 64 / kLanes;
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = first + (int64_t)blockIdx.x * (kJoinThreads / 64) + (threadIdx.x >> 6), sequence = unit / p.heads;
+    if (unit >= units) return;
+    const SplitRange range = range_of(p, sequence);
+    if (range.used <= 1) return;
+    const float* ml = p.part_ml + unit * p.splits * 2;
+    const bool there = lane < range.used;
+    const float m = there ? ml[2 * lane] : attend::kNothing, l = there ? ml[2 * lane + 1] : 0.0f;
+    const float top = wave_max(m), f = attend::power2(m - top);
+    float sum = f * l;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+    const int col = lane % kLanes, group = lane / kLanes;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o + unit * p.splits * D) + col;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int from = 0; from < range.used; from += kGroups) {
+        const int i = from + group;
+        const float w = __shfl(f, i & 63, 64);
+        if (group < kGroups && i < range.used) add4(a, o[(int64_t)i * kLanes], w);
+    }
+    float4 all = a;
+#pragma unroll
+    for (int i = 1; i < kGroups; i++) {
+        all.x += __shfl(a.x, col + i * kLanes, 64), all.y += __shfl(a.y, col + i * kLanes, 64);
+        all.z += __shfl(a.z, col + i * kLanes, 64), all.w += __shfl(a.w, col + i * kLanes, 64);
+    }
+    if (lane < kLanes) {
+        put_joined(p, unit, sequence, D, 4 * col, all.x, sum);
+        put_joined(p, unit, sequence, D, 4 * col + 1, all.y, sum);
+        put_joined(p, unit, sequence, D, 4 * col + 2, all.z, sum);
+        put_joined(p, unit, sequence, D, 4 * col + 3, all.w, sum);
+        if (lane == 0) put_lse(p, unit, top, sum);
+    }
+}
+
+namespace {
+
+template <int D>
+hipError_t join(const AttendParams& p, hipStream_t s) {
+    const int64_t units = p.sequences * p.heads;
+    const bool few = p.splits <= kFewParts;
+    const int64_t each = few ? kJoinThreads / 64 : 1, most = max_workgroups(kJoinThreads) * each;
+    for (int64_t first = 0; first < units; first += most) {
+        const int64_t n = units - first < most ? units - first : most;
+        const dim3 grid((unsigned)((n + each - 1) / each));
+        if (few) attend_join_few_kernel<D><<<grid, kJoinThreads, 0, s>>>(p, first, units);
+        else attend_join_kernel<D><<<grid, kJoinThreads, 0, s>>>(p, first, units);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
 
 hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
     hipError_t e;
@@ -79,19 +150,13 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
         default: e = launch_attend_bf16(p, s); break;
     }
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t units = p.sequences * p.heads, most = max_workgroups(kJoinThreads);
-    for (int64_t first = 0; first < units; first += most) {
-        const dim3 grid((unsigned)(units - first < most ? units - first : most));
-        switch (p.c.head_dim) {
-            case 64: attend_join_kernel<64><<<grid, kJoinThreads, 0, s>>>(p, first); break;
-            case 96: attend_join_kernel<96><<<grid, kJoinThreads, 0, s>>>(p, first); break;
-            case 128: attend_join_kernel<128><<<grid, kJoinThreads, 0, s>>>(p, first); break;
-            case 192: attend_join_kernel<192><<<grid, kJoinThreads, 0, s>>>(p, first); break;
-            default: attend_join_kernel<256><<<grid, kJoinThreads, 0, s>>>(p, first); break;
-        }
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+    switch (p.c.head_dim) {
+        case 64: return join<64>(p, s);
+        case 96: return join<96>(p, s);
+        case 128: return join<128>(p, s);
+        case 192: return join<192>(p, s);
+        default: return join<256>(p, s);
     }
-    return hipSuccess;
 }
 
 }  // namespace fp4

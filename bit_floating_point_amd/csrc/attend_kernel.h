@@ -35,8 +35,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = kAttendWaves * 64;
-constexpr float kNothing = -3.0e38f;  // the maximum where no position was seen
-constexpr float kSlack = 8.0f;        // z may pass m by this: weights to 2^8
+constexpr float kNothing = -3.0e38f;  // z of a position that is not seen; m before the first
+constexpr float kSlack = 8.0f;        // log2 of the largest weight: z may pass m by this much
 
 // `total` things in pieces of powers of two, none above `most`: number, start and size
 constexpr int piece_size(int total, int most, int l) {
@@ -154,6 +154,7 @@ __device__ __forceinline__ void terms_of(float x[8], bf16x8 out[N]) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+            asm("" : "+v"(w[i]));  // the pair is at hand: its halves are not converted again
             x[2 * i] -= low_half(w[i]);
             x[2 * i + 1] -= high_half(w[i]);
         }
@@ -191,9 +192,16 @@ struct RowScales {
     }
 };
 
+// Wavefronts per SIMD that a kernel has registers for, at least.  Two: with no more than 256
+// registers the matrix instructions keep their sums in ordinary ones, where O is scaled in place
+// (ragged E2M1 113 -> 101 us).  Rows of 256 fit those only in few bits, or with one term of q.
+constexpr int least_waves(int store, int dim, bool wide) {
+    return dim == 256 && (store == kStoreBf16 || (wide && store != kStoreE2m1)) ? 1 : 2;
+}
+
 // WIDE: q or y is f32, and its terms three.
 template <int STORE, int SCALES, int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_t first_sequence) {
+__global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_kernel(AttendParams p, int64_t first_sequence) {
     using L = Plan<STORE, D>;
     constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
     constexpr int kRound = 8;  // heads whose parts are joined at a time
@@ -223,6 +231,17 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
     const int all = (end - begin + kTilePositions - 1) / kTilePositions;  // tiles of the part
     const int count = (all - wave + kAttendWaves - 1) / kAttendWaves;     // of this wavefront (at most 0: none)
 
+    // z = dot * (row's scale) * factor, factor >= 0: a negative one changes q's sign
+    constexpr bool kRows = SCALES != kScaleNone;
+    float factor = p.scale_log2, v_all = 1.0f;
+    if (c.scales == kScaleGiven) {
+        factor *= *reinterpret_cast<const float*>(c.k_scales);
+        v_all = *reinterpret_cast<const float*>(c.v_scales);
+    }
+    const float sign = factor < 0.0f ? -1.0f : 1.0f;
+    factor *= sign;
+    const float slack = kSlack / factor;
+
     // q of head n, in K's order of columns
     bf16x8 q[kQTerms][L::kSteps];
     {
@@ -234,6 +253,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
             for (int i = 0; i < steps; i++) {
                 float x[8] = {};
                 if (there) get8(p.q, p.q_bf16, row + first * 32 + g * 8 * steps + 8 * i, x);
+#pragma unroll
+                for (int e = 0; e < 8; e++) x[e] *= sign;
                 bf16x8 t[kQTerms];
                 terms_of<kQTerms>(x, t);
 #pragma unroll
@@ -242,62 +263,71 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
         });
     }
 
-    float m = kNothing, l = 0.0f;
+    // m: the reference, times factor; dots (with the rows' scales) past `bar` move it
+    float m = kNothing, bar = kNothing, l = 0.0f;
     f32x4 acc[L::kCols];
 #pragma unroll
     for (int j = 0; j < L::kCols; j++) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     uint32_t kw[2][L::kWords], vw[8][L::vWords];
-    constexpr bool kRows = SCALES != kScaleNone;
     RowScales<SCALES> ks, vs;
-    float k_all = p.scale_log2, v_all = 1.0f;
-    if (c.scales == kScaleGiven) {
-        k_all *= *reinterpret_cast<const float*>(c.k_scales);
-        v_all = *reinterpret_cast<const float*>(c.v_scales);
-    }
 
-    // The pages of 32 of this wavefront's tiles, one half of a tile a lane; -1: not there.
+    // Where the halves of 32 of this wavefront's tiles lie, one half a lane: the byte offset of the first
+    // of the 16 rows and the index of its scale.  A half that is not in the cache or has nothing
+    // to be seen: page 0 in its place, read and not used, and the highest bit set.
     const int32_t* table = p.table + sequence * p.ld_table;
-    int page_ids = -1;
+    const int slots = (1 << c.page_log) - 1;
+    constexpr uint32_t kAbsent = 0x80000000u;
+    uint32_t row_low = 0, row_high = 0, scale_low = 0, scale_high = 0;
     auto find_pages = [&](int i) {
         const int t = begin + ((i + (lane >> 1)) * kAttendWaves + wave) * kTilePositions + 16 * (lane & 1);
-        page_ids = t < end ? page_at(table + (t >> c.page_log), c.pages) : -1;
+        const int found = t < end ? page_at(table + (t >> c.page_log), c.pages) : -1, page = max(found, 0);
+        const int64_t row = page * c.stride_page + kv_head * c.stride_head + (int64_t)(t & slots) * c.stride_row;
+        row_low = (uint32_t)row;
+        row_high = (uint32_t)(row >> 32) | (found < 0 ? kAbsent : 0);
+        if constexpr (kRows) {
+            const int64_t scale = (((int64_t)page * c.kv_heads + kv_head) << c.page_log) + (t & slots);
+            scale_low = (uint32_t)scale;
+            scale_high = (uint32_t)(scale >> 32);
+        }
     };
-    // a tile of this wavefront: its first position and its halves' pages (-1: nothing there to
-    // be seen; page 0 is read in its place and not used)
+    // a tile of this wavefront: its first position, and where its halves lie
     struct Tile {
-        int t, page[2];
+        int t;
+        bool there[2];
+        int64_t row[2], scale[2];
     };
     auto tile_of = [&](int i) {
         Tile r;
         r.t = begin + (i * kAttendWaves + wave) * kTilePositions;
-        r.page[0] = __builtin_amdgcn_readlane(page_ids, 2 * (i & 31));
-        r.page[1] = __builtin_amdgcn_readlane(page_ids, 2 * (i & 31) + 1);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int from = 2 * (i & 31) + h;
+            const uint32_t high = __builtin_amdgcn_readlane(row_high, from);
+            r.there[h] = (high & kAbsent) == 0;
+            r.row[h] = (int64_t)(((uint64_t)(high & ~kAbsent) << 32) | (uint32_t)__builtin_amdgcn_readlane(row_low, from));
+            if constexpr (kRows)
+                r.scale[h] = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(scale_high, from) << 32) |
+                                       (uint32_t)__builtin_amdgcn_readlane(scale_low, from));
+        }
         return r;
-    };
-    const int slots = (1 << c.page_log) - 1;
-    auto half_base = [&](const Tile& tile, int h) {
-        return max(tile.page[h], 0) * c.stride_page + kv_head * c.stride_head + (int64_t)((tile.t + 16 * h) & slots) * c.stride_row;
-    };
-    auto half_scales = [&](const Tile& tile, int h) {
-        return (((int64_t)max(tile.page[h], 0) * c.kv_heads + kv_head) << c.page_log) + ((tile.t + 16 * h) & slots);
     };
     const uint32_t key_row = (uint32_t)n * c.stride_row, value_row = (uint32_t)(4 * g) * c.stride_row;
     auto load_keys = [&](const Tile& tile) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const auto rows = buffer_at(c.k, half_base(tile, h));
+            const auto rows = buffer_at(c.k, tile.row[h]);
             repeat<L::kLoads>([&](auto x) {
                 constexpr int first = L::k_first(x), steps = L::k_steps(x), bytes = steps * L::kStepBytes;
                 load_bytes<bytes>(rows, key_row + (uint32_t)(first * 4 * L::kStepBytes + g * bytes), 0, kw[h] + first * L::kStepBytes / 4);
             });
-            ks.load(c.k_scales, half_scales(tile, h), h, g);
+            ks.load(c.k_scales, tile.scale[h], h, g);
         }
     };
     auto load_values = [&](const Tile& tile) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const auto rows = buffer_at(c.v, half_base(tile, h));
+            const auto rows = buffer_at(c.v, tile.row[h]);
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 repeat<L::vLoads>([&](auto x) {
@@ -305,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
                     load_bytes<bytes>(rows, value_row + (uint32_t)(L::v_first(x) * 2 * L::kBits + n * bytes), (uint32_t)j * c.stride_row,
                                       vw[4 * h + j] + L::v_word_first(x));
                 });
-            vs.load(c.v_scales, half_scales(tile, h), h, g);
+            vs.load(c.v_scales, tile.scale[h], h, g);
         }
     };
 
@@ -334,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
         }
         float z[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) z[j] = z2[j / 4][j % 4] * (kRows ? ks.get(j) * k_all : k_all);
+        for (int j = 0; j < 8; j++) z[j] = kRows ? z2[j / 4][j % 4] * ks.get(j) : z2[j / 4][j % 4];
         Tile next{};
         if constexpr (more) {
             if (((i + 1) & 31) == 0) find_pages(i + 1);
@@ -343,28 +373,29 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p, int64_
         }
         // what is not seen: no weight, whatever its rows and scales hold
         bool seen[8];
-        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && tile.page[0] >= 0 && tile.page[1] >= 0;
+        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && tile.there[0] && tile.there[1];
         if (!whole) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
-                seen[j] = t >= range.begin && t < end && tile.page[j / 4] >= 0;
+                seen[j] = (t >= range.begin) & (t < end) & tile.there[j / 4];
                 z[j] = seen[j] ? z[j] : kNothing;
             }
         }
         float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
-        if (__any(top > m + kSlack)) {
+        if (__any(top > bar)) {
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float to = fmaxf(m, top), f = power2(m - to);
+            const float to = fmaxf(m, top * factor), f = power2(m - to);
             m = to;
+            bar = fmaxf(bar, top + slack);
             l *= f;
 #pragma unroll
             for (int j = 0; j < L::kCols; j++) acc[j] *= f;
         }
         float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = power2(z[j] - m);
+        for (int j = 0; j < 8; j++) w[j] = power2(__builtin_fmaf(z[j], factor, -m));
         if (!whole) {
 #pragma unroll
             for (int j = 0; j < 8; j++) w[j] = seen[j] ? w[j] : 0.0f;
