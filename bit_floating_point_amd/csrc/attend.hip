@@ -28,18 +28,15 @@ __device__ __forceinline__ float block_reduce(float v, float* part, bool largest
 
 }  // namespace
 
-// one value of the result: column `col` of head `unit`, O over the sum of weights
-__device__ __forceinline__ void put_joined(const AttendParams& p, int64_t unit, int64_t sequence, int dim, int col, float o, float sum) {
-    const float y = sum > 0.0f ? o / sum : sum == 0.0f ? 0.0f : sum;
-    const int64_t to = sequence * p.ldy + (unit - sequence * p.heads) * dim + col;
-    if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[to] = (__bf16)y;
-    else reinterpret_cast<float*>(p.y)[to] = y;
-}
-__device__ __forceinline__ void put_lse(const AttendParams& p, int64_t unit, float top, float sum) {
-    if (p.lse) p.lse[unit] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0x1.62e43p-1f;
+// four columns of the result of head `unit`: O over the sum of weights
+__device__ __forceinline__ void put_joined(const AttendParams& p, int64_t unit, int64_t sequence, int dim, int col, const float4& o, float top,
+                                           float sum) {
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    attend::put4(p.y, p.y_bf16, sequence * p.ldy + (unit - sequence * p.heads) * dim + col, attend::f32x4{o.x * f, o.y * f, o.z * f, o.w * f});
+    if (p.lse && col == 0) p.lse[unit] = attend::log_sum(top, sum);
 }
 __device__ __forceinline__ SplitRange range_of(const AttendParams& p, int64_t sequence) {
-    return split_range(max(0, min(p.lengths[sequence], p.capacity)), p.window, p.splits);
+    return split_range(max(0, min(p.lengths[sequence], p.capacity)), p.window, p.split_log);
 }
 __device__ __forceinline__ void add4(float4& a, const float4& v, float w) {
     a.x = __builtin_fmaf(v.x, w, a.x), a.y = __builtin_fmaf(v.y, w, a.y);
@@ -55,9 +52,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams 
     __shared__ float4 sums[kGroups][kLanes];
     const int64_t unit = first + blockIdx.x, sequence = unit / p.heads;
     const SplitRange range = range_of(p, sequence);
-    if (range.used <= 1) return;
+    const int used = range.used();
+    if (used <= 1) return;
     const float* ml = p.part_ml + unit * p.splits * 2;
-    const bool there = (int)threadIdx.x < range.used;
+    const bool there = (int)threadIdx.x < used;
     const float m = there ? ml[2 * threadIdx.x] : attend::kNothing, l = there ? ml[2 * threadIdx.x + 1] : 0.0f;
     const float top = block_reduce(m, part[0], true);
     const float f = attend::power2(m - top);
@@ -68,16 +66,15 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendParams 
         const float4* o = reinterpret_cast<const float4*>(p.part_o + unit * p.splits * D) + col;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int i = group; i < range.used; i += kGroups) add4(a, o[(int64_t)i * kLanes], weight[i]);
+        for (int i = group; i < used; i += kGroups) add4(a, o[(int64_t)i * kLanes], weight[i]);
         sums[group][col] = a;
     }
     __syncthreads();
-    if (threadIdx.x < D) {
-        float o = 0.0f;
+    if (threadIdx.x < kLanes) {
+        float4 o = sums[0][threadIdx.x];
 #pragma unroll
-        for (int i = 0; i < kGroups; i++) o += reinterpret_cast<const float*>(&sums[i][0])[threadIdx.x];
-        put_joined(p, unit, sequence, D, threadIdx.x, o, sum);
-        if (threadIdx.x == 0) put_lse(p, unit, top, sum);
+        for (int i = 1; i < kGroups; i++) add4(o, sums[i][threadIdx.x], 1.0f);
+        put_joined(p, unit, sequence, D, 4 * threadIdx.x, o, top, sum);
     }
 }
 
@@ -89,9 +86,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_few_kernel(AttendPar
     const int64_t unit = first + (int64_t)blockIdx.x * (kJoinThreads / 64) + (threadIdx.x >> 6), sequence = unit / p.heads;
     if (unit >= units) return;
     const SplitRange range = range_of(p, sequence);
-    if (range.used <= 1) return;
+    const int used = range.used();
+    if (used <= 1) return;
     const float* ml = p.part_ml + unit * p.splits * 2;
-    const bool there = lane < range.used;
+    const bool there = lane < used;
     const float m = there ? ml[2 * lane] : attend::kNothing, l = there ? ml[2 * lane + 1] : 0.0f;
     const float top = wave_max(m), f = attend::power2(m - top);
     float sum = f * l;
@@ -101,10 +99,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_few_kernel(AttendPar
     const float4* o = reinterpret_cast<const float4*>(p.part_o + unit * p.splits * D) + col;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int from = 0; from < range.used; from += kGroups) {
+    for (int from = 0; from < used; from += kGroups) {
         const int i = from + group;
         const float w = __shfl(f, i & 63, 64);
-        if (group < kGroups && i < range.used) add4(a, o[(int64_t)i * kLanes], w);
+        if (group < kGroups && i < used) add4(a, o[(int64_t)i * kLanes], w);
     }
     float4 all = a;
 #pragma unroll
@@ -112,13 +110,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_few_kernel(AttendPar
         all.x += __shfl(a.x, col + i * kLanes, 64), all.y += __shfl(a.y, col + i * kLanes, 64);
         all.z += __shfl(a.z, col + i * kLanes, 64), all.w += __shfl(a.w, col + i * kLanes, 64);
     }
-    if (lane < kLanes) {
-        put_joined(p, unit, sequence, D, 4 * col, all.x, sum);
-        put_joined(p, unit, sequence, D, 4 * col + 1, all.y, sum);
-        put_joined(p, unit, sequence, D, 4 * col + 2, all.z, sum);
-        put_joined(p, unit, sequence, D, 4 * col + 3, all.w, sum);
-        if (lane == 0) put_lse(p, unit, top, sum);
-    }
+    if (lane < kLanes) put_joined(p, unit, sequence, D, 4 * col, all, top, sum);
 }
 
 namespace {

@@ -164,6 +164,18 @@ __device__ __forceinline__ void terms_of(float x[8], bf16x8 out[N]) {
 
 __device__ __forceinline__ float power2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// the logarithm of a sum of exponentials: 2^m times `sum`
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0x1.62e43p-1f; }
+
+// four values into a row of f32 or bf16
+__device__ __forceinline__ void put4(void* base, bool bf16, int64_t at, const f32x4& v) {
+    if (bf16) *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(base) + at) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(base) + at) = v;
+}
+
+// v is used here, so that its load is waited for here
+__device__ __forceinline__ void arrived(bf16x8& v) { asm volatile("" : "+v"(v)); }
+
 // f(integral_constant<0>) .. f(integral_constant<N - 1>)
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void repeat(F&& f) {
@@ -184,19 +196,20 @@ struct RowScales {
     __device__ __forceinline__ void load(const void* scales, int64_t first, int half, int g) {
         if constexpr (kBytes) load_bytes<4 * kBytes>(buffer_at(scales, first * kBytes), (uint32_t)(4 * g * kBytes), 0, w[half]);
     }
-    __device__ __forceinline__ float get(int j) const {
+    // x * (row j's scale) + y, rounded once: one instruction, binary16 scales are converted inside it
+    __device__ __forceinline__ float fma(int j, float x, float y) const {
         const uint32_t* h = w[j / 4];
-        if constexpr (SCALES == kScaleRowF32) return __uint_as_float(h[j % 4]);
-        else if constexpr (SCALES == kScaleRowF16) return __half2float(__ushort_as_half((uint16_t)(h[j % 4 / 2] >> (16 * (j % 2)))));
-        else return 1.0f;
+        if constexpr (SCALES == kScaleRowF32) return __builtin_fmaf(x, __uint_as_float(h[j % 4]), y);
+        else return __builtin_fmaf(x, (float)__builtin_bit_cast(_Float16, (uint16_t)(h[j % 4 / 2] >> (16 * (j % 2)))), y);
     }
 };
 
 // Wavefronts per SIMD that a kernel has registers for, at least.  Two: with no more than 256
 // registers the matrix instructions keep their sums in ordinary ones, where O is scaled in place
-// (ragged E2M1 113 -> 101 us).  Rows of 256 fit those only in few bits, or with one term of q.
+// (ragged E2M1 113 -> 101 us).  The widest rows do not fit those.
 constexpr int least_waves(int store, int dim, bool wide) {
-    return dim == 256 && (store == kStoreBf16 || (wide && store != kStoreE2m1)) ? 1 : 2;
+    const bool bf16 = store == kStoreBf16;
+    return (dim == 256 && (bf16 || (wide && store != kStoreE2m1))) || (dim == 192 && bf16 && wide) ? 1 : 2;
 }
 
 // WIDE: q or y is f32, and its terms three.
@@ -206,41 +219,34 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
     constexpr int kRound = 8;  // heads whose parts are joined at a time
     __shared__ float joined[kAttendWaves][kRound][D + 4];
-    __shared__ float stats[kAttendWaves][kHeadTile][2];
+    __shared__ float2 stats[kAttendWaves][kHeadTile];
 
     const CacheParams& c = p.c;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // workgroup -> sequence, kv head, tile of its query heads, part
+    // workgroup (part, kv head and tile of its query heads, sequence)
     const uint32_t tiles = (uint32_t)(p.share + kHeadTile - 1) / kHeadTile;
-    uint32_t at = blockIdx.x;
-    const int split = (int)(at % (uint32_t)p.splits);
-    at /= (uint32_t)p.splits;
-    const int head_tile = (int)(at % tiles);
-    at /= tiles;
-    const int kv_head = (int)(at % (uint32_t)c.kv_heads);
-    const int64_t sequence = first_sequence + at / (uint32_t)c.kv_heads;
+    const int split = (int)blockIdx.x, kv_head = (int)(tiles == 1 ? blockIdx.y : blockIdx.y / tiles);
+    const int head_tile = (int)(blockIdx.y - (uint32_t)kv_head * tiles);
+    const int64_t sequence = first_sequence + blockIdx.z;
     const int heads = min(p.share - head_tile * kHeadTile, kHeadTile);  // of this tile
     const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeadTile;
 
     const int32_t length = __builtin_amdgcn_readfirstlane(max(0, min(p.lengths[sequence], p.capacity)));
-    const SplitRange range = split_range(length, p.window, p.splits);
-    if (split > 0 && split >= range.used) return;
+    const SplitRange range = split_range(length, p.window, p.split_log);
+    if (split > 0 && !range.has(split)) return;
     const int begin = range.first + split * range.chunk;
     const int end = length - begin < range.chunk ? length : begin + range.chunk;
     const int all = (end - begin + kTilePositions - 1) / kTilePositions;  // tiles of the part
     const int count = (all - wave + kAttendWaves - 1) / kAttendWaves;     // of this wavefront (at most 0: none)
 
-    // z = dot * (row's scale) * factor, factor >= 0: a negative one changes q's sign
+    // z = dot * factor * (row's scale)
     constexpr bool kRows = SCALES != kScaleNone;
     float factor = p.scale_log2, v_all = 1.0f;
     if (c.scales == kScaleGiven) {
         factor *= *reinterpret_cast<const float*>(c.k_scales);
         v_all = *reinterpret_cast<const float*>(c.v_scales);
     }
-    const float sign = factor < 0.0f ? -1.0f : 1.0f;
-    factor *= sign;
-    const float slack = kSlack / factor;
 
     // q of head n, in K's order of columns
     bf16x8 q[kQTerms][L::kSteps];
@@ -251,23 +257,26 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
             constexpr int first = L::k_first(l), steps = L::k_steps(l);
 #pragma unroll
             for (int i = 0; i < steps; i++) {
-                float x[8] = {};
-                if (there) get8(p.q, p.q_bf16, row + first * 32 + g * 8 * steps + 8 * i, x);
+                const int64_t col = row + first * 32 + g * 8 * steps + 8 * i;
+                if constexpr (WIDE) {
+                    float x[8] = {};
+                    if (there) get8(p.q, p.q_bf16, col, x);
+                    bf16x8 t[kQTerms];
+                    terms_of<kQTerms>(x, t);
 #pragma unroll
-                for (int e = 0; e < 8; e++) x[e] *= sign;
-                bf16x8 t[kQTerms];
-                terms_of<kQTerms>(x, t);
-#pragma unroll
-                for (int k = 0; k < kQTerms; k++) q[k][first + i] = t[k];
+                    for (int k = 0; k < kQTerms; k++) q[k][first + i] = t[k];
+                } else {
+                    q[0][first + i] = bf16x8{};
+                    if (there) q[0][first + i] = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const uint16_t*>(p.q) + col);
+                }
             }
         });
     }
 
-    // m: the reference, times factor; dots (with the rows' scales) past `bar` move it
-    float m = kNothing, bar = kNothing, l = 0.0f;
+    float m = 0.0f, l = 0.0f;
+    bool fresh = true;  // nothing was seen yet
     f32x4 acc[L::kCols];
-#pragma unroll
-    for (int j = 0; j < L::kCols; j++) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    repeat<L::kCols>([&](auto j) { acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
 
     uint32_t kw[2][L::kWords], vw[8][L::vWords];
     RowScales<SCALES> ks, vs;
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     // a tile of this wavefront: its first position, and where its halves lie
     struct Tile {
         int t;
-        bool there[2];
+        uint32_t high[2];  // kAbsent
         int64_t row[2], scale[2];
     };
     auto tile_of = [&](int i) {
@@ -303,9 +312,8 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const int from = 2 * (i & 31) + h;
-            const uint32_t high = __builtin_amdgcn_readlane(row_high, from);
-            r.there[h] = (high & kAbsent) == 0;
-            r.row[h] = (int64_t)(((uint64_t)(high & ~kAbsent) << 32) | (uint32_t)__builtin_amdgcn_readlane(row_low, from));
+            r.high[h] = __builtin_amdgcn_readlane(row_high, from);
+            r.row[h] = (int64_t)(((uint64_t)(r.high[h] & ~kAbsent) << 32) | (uint32_t)__builtin_amdgcn_readlane(row_low, from));
             if constexpr (kRows)
                 r.scale[h] = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(scale_high, from) << 32) |
                                        (uint32_t)__builtin_amdgcn_readlane(scale_low, from));
@@ -331,97 +339,99 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 repeat<L::vLoads>([&](auto x) {
-                    constexpr int bytes = L::v_bytes(x);
-                    load_bytes<bytes>(rows, value_row + (uint32_t)(L::v_first(x) * 2 * L::kBits + n * bytes), (uint32_t)j * c.stride_row,
-                                      vw[4 * h + j] + L::v_word_first(x));
+                    constexpr int bytes = L::v_bytes(x), first = L::v_first(x), word = L::v_word_first(x);
+                    load_bytes<bytes>(rows, value_row + (uint32_t)(first * 2 * L::kBits + n * bytes), (uint32_t)j * c.stride_row,
+                                      vw[4 * h + j] + word);
                 });
             vs.load(c.v_scales, tile.scale[h], h, g);
         }
     };
 
     Tile tile{};
-    if (count > 0) {
-        find_pages(0);
-        tile = tile_of(0);
-        load_keys(tile);
-        load_values(tile);
-    }
-    // Tile i; with `more`, the loads of tile i + 1 start where the registers of i's keys and then of its
-    // values are free.  (The last tile is a copy of its own: a load under a condition would be
-    // waited for where the condition ends.)
+    // Tile i.  `more`: the loads of tile i + 1 start where the registers of i's keys and then of its values
+    // are free.  (The last tile is a copy of its own: a load under a condition would be waited for
+    // where the condition ends.)
     auto step = [&](int i, auto more) {
         // Z^T of both halves
         f32x4 z2[2];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            z2[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int h = 0; h < 2; h++) z2[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < L::kSteps; s++) {
+        for (int s = 0; s < L::kSteps; s++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
                 const bf16x8 a = key_operand<STORE>(kw[h] + s * L::kStepBytes / 4);
 #pragma unroll
                 for (int k = kQTerms - 1; k >= 0; k--) z2[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z2[h], 0, 0, 0);
             }
-        }
-        float z[8];
+        // x = z - m
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) z[j] = kRows ? z2[j / 4][j % 4] * ks.get(j) : z2[j / 4][j % 4];
+        for (int j = 0; j < 8; j++) {
+            const float dot = z2[j / 4][j % 4];
+            if constexpr (kRows) x[j] = ks.fma(j, dot * factor, -m);
+            else x[j] = __builtin_fmaf(dot, factor, -m);
+        }
         Tile next{};
         if constexpr (more) {
             if (((i + 1) & 31) == 0) find_pages(i + 1);
             next = tile_of(i + 1);
             load_keys(next);
         }
-        // what is not seen: no weight, whatever its rows and scales hold
-        bool seen[8];
-        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && tile.there[0] && tile.there[1];
-        if (!whole) {
+        // What is not seen has no weight, whatever its rows and scales hold.  (It may call for a new
+        // reference in vain.)
+        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && (int)(tile.high[0] | tile.high[1]) >= 0;
+        auto seen = [&](int j) {
+            const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
+            return whole | ((t >= range.begin) & (t < end) & ((int)tile.high[j / 4] >= 0));
+        };
+        const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        if (fresh | __any(most > kSlack)) {
+            float top = kNothing;
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
-                seen[j] = (t >= range.begin) & (t < end) & tile.there[j / 4];
-                z[j] = seen[j] ? z[j] : kNothing;
-            }
-        }
-        float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
-        if (__any(top > bar)) {
+            for (int j = 0; j < 8; j++) top = fmaxf(top, seen(j) ? x[j] : kNothing);
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float to = fmaxf(m, top * factor), f = power2(m - to);
-            m = to;
-            bar = fmaxf(bar, top + slack);
+            // m moves to the first tile's largest z that has any (it was 0 until then), then upwards
+            const bool none = __all(top <= kNothing);
+            top = none ? 0.0f : fresh ? top : fmaxf(top, 0.0f);
+            const float f = fresh ? 1.0f : power2(-top);
+            fresh &= none;
+            m += top;
             l *= f;
+            repeat<L::kCols>([&](auto j) { acc[j] *= f; });
 #pragma unroll
-            for (int j = 0; j < L::kCols; j++) acc[j] *= f;
+            for (int j = 0; j < 8; j++) x[j] -= top;
         }
-        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = power2(__builtin_fmaf(z[j], factor, -m));
+        for (int j = 0; j < 8; j++) x[j] = power2(x[j]);
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) w[j] = seen[j] ? w[j] : 0.0f;
+            for (int j = 0; j < 8; j++) x[j] = seen(j) ? x[j] : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            l += w[j];
-            if constexpr (kRows) w[j] *= vs.get(j);
+            l += x[j];
+            if constexpr (kRows) x[j] = vs.fma(j, x[j], 0.0f);
         }
         if (!whole) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                if constexpr (kRows) w[j] = seen[j] ? w[j] : 0.0f;
+                if constexpr (kRows) x[j] = seen(j) ? x[j] : 0.0f;
 #pragma unroll
-                for (int u = 0; u < L::vWords; u++) vw[j][u] = seen[j] ? vw[j][u] : 0u;
+                for (int u = 0; u < L::vWords; u++) vw[j][u] = seen(j) ? vw[j][u] : 0u;
             }
         }
         bf16x8 weight[kPTerms];
-        terms_of<kPTerms>(w, weight);
+        terms_of<kPTerms>(x, weight);
         // O^T: a column of V at a time
-        repeat<L::vLoads>([&](auto x) {
-            repeat<L::v_cols(x)>([&](auto e) {
-                constexpr int per = 32 / L::kBits, word = L::v_word_first(x) + e / per;
+        repeat<L::vLoads>([&](auto y) {
+            repeat<L::v_cols(y)>([&](auto e) {
+                constexpr int per = 32 / L::kBits, word = L::v_word_first(y) + e / per;
                 const bf16x8 a = operand(value_pair<STORE, e % per>(vw[0][word], vw[1][word]), value_pair<STORE, e % per>(vw[2][word], vw[3][word]),
                                          value_pair<STORE, e % per>(vw[4][word], vw[5][word]), value_pair<STORE, e % per>(vw[6][word], vw[7][word]));
-                f32x4& o = acc[L::v_first(x) + e];
+                constexpr int col = L::v_first(y) + e;
+                f32x4& o = acc[col];
 #pragma unroll
                 for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[k], o, 0, 0, 0);
             });
@@ -431,17 +441,40 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
             tile = next;
         }
     };
-    for (int i = 0; i + 1 < count; i++) step(i, std::true_type{});
-    if (count > 0) step(count - 1, std::false_type{});
+    if (count > 0) {
+        find_pages(0);
+        tile = tile_of(0);
+        load_keys(tile);
+        load_values(tile);
+        // q is waited for here, beside those: in the loop it would be waited for, with all loads, in every turn
+#pragma unroll
+        for (int k = 0; k < kQTerms; k++)
+#pragma unroll
+            for (int s = 0; s < L::kSteps; s++) arrived(q[k][s]);
+        for (int i = 0; i + 1 < count; i++) step(i, std::true_type{});
+        step(count - 1, std::false_type{});
+    }
+    if (fresh) m = kNothing;
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
 
-    // the wavefronts' parts, joined; lane (n, g) holds columns first * 16 + cols (4 g + i) + e
-    if (g == 0) {
-        stats[wave][n][0] = m;
-        stats[wave][n][1] = l;
+    // The wavefronts' parts, joined: each scales its own O to the largest m (and over the sum, if this is the
+    // only part), then they are added in order.  Lane (n, g) holds columns first * 16 + cols (4 g + i) + e.
+    if (g == 0) stats[wave][n] = make_float2(m, l);
+    __syncthreads();
+    float top = stats[0][n].x, sum = 0.0f;
+#pragma unroll
+    for (int v = 1; v < kAttendWaves; v++) top = fmaxf(top, stats[v][n].x);
+#pragma unroll
+    for (int v = 0; v < kAttendWaves; v++) sum = __builtin_fmaf(stats[v][n].y, power2(stats[v][n].x - top), sum);
+    const bool alone = range.count <= range.chunk;
+    float own = power2(m - top) * v_all;
+    if (alone) own *= sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t head = sequence * p.heads + first_head;  // of n = 0
+    if (wave == 0 && g == 0 && n < heads) {
+        if (!alone) *reinterpret_cast<float2*>(p.part_ml + ((head + n) * p.splits + split) * 2) = make_float2(top, sum);
+        else if (p.lse) p.lse[head + n] = log_sum(top, sum);
     }
-    const int64_t unit = sequence * p.heads + first_head;
     for (int r = 0; r < heads; r += kRound) {
         if (r > 0) __syncthreads();
         if (n >= r && n < r + kRound) {
@@ -449,38 +482,18 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
                 repeat<L::v_cols(x)>([&](auto e) {
                     constexpr int cols = L::v_cols(x), first = L::v_first(x);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) joined[wave][n - r][first * 16 + cols * (4 * g + i) + e] = acc[first + e][i];
+                    for (int i = 0; i < 4; i++) joined[wave][n - r][first * 16 + cols * (4 * g + i) + e] = acc[first + e][i] * own;
                 });
             });
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < min(heads - r, kRound) * D; e += kThreads) {
+        for (int e = threadIdx.x * 4; e < min(heads - r, kRound) * D; e += kThreads * 4) {
             const int row = e / D, col = e % D;
-            float top = stats[0][r + row][0];
+            f32x4 o = *reinterpret_cast<const f32x4*>(&joined[0][row][col]);
 #pragma unroll
-            for (int v = 1; v < kAttendWaves; v++) top = fmaxf(top, stats[v][r + row][0]);
-            float sum = 0.0f, o = 0.0f;
-#pragma unroll
-            for (int v = 0; v < kAttendWaves; v++) {
-                const float f = power2(stats[v][r + row][0] - top);
-                sum = __builtin_fmaf(stats[v][r + row][1], f, sum);
-                o = __builtin_fmaf(joined[v][row][col], f, o);
-            }
-            o *= v_all;
-            const int64_t head = unit + r + row;
-            if (range.used > 1) {
-                p.part_o[(head * p.splits + split) * D + col] = o;
-                if (col == 0) {
-                    p.part_ml[(head * p.splits + split) * 2] = top;
-                    p.part_ml[(head * p.splits + split) * 2 + 1] = sum;
-                }
-            } else {
-                const float y = sum > 0.0f ? o / sum : sum == 0.0f ? 0.0f : sum;
-                const int64_t to = sequence * p.ldy + (first_head + r + row) * D + col;
-                if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[to] = (__bf16)y;
-                else reinterpret_cast<float*>(p.y)[to] = y;
-                if (p.lse && col == 0) p.lse[head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0x1.62e43p-1f;
-            }
+            for (int v = 1; v < kAttendWaves; v++) o += *reinterpret_cast<const f32x4*>(&joined[v][row][col]);
+            if (!alone) *reinterpret_cast<f32x4*>(p.part_o + ((head + r + row) * p.splits + split) * D + col) = o;
+            else put4(p.y, p.y_bf16, sequence * p.ldy + (first_head + r + row) * D + col, o);
         }
     }
 }
@@ -489,11 +502,12 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
 template <int STORE>
 hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
     const bool wide = !p.q_bf16 || !p.y_bf16;
-    const int64_t tiles = (p.share + kHeadTile - 1) / kHeadTile, each = (int64_t)p.c.kv_heads * tiles * p.splits;
-    const int64_t most = max_workgroups(kThreads) / each;
+    const int64_t units = (int64_t)p.c.kv_heads * ((p.share + kHeadTile - 1) / kHeadTile);
+    int64_t most = max_workgroups(kThreads) / (units * p.splits);
+    if (most > 65535) most = 65535;  // of a grid's third dimension
     for (int64_t first = 0; first < p.sequences; first += most) {
         const int64_t n = p.sequences - first < most ? p.sequences - first : most;
-        const dim3 grid((unsigned)(n * each));
+        const dim3 grid((unsigned)p.splits, (unsigned)units, (unsigned)n);
         auto with = [&](auto dim, auto scales) {
             constexpr int D = decltype(dim)::value, SCALES = decltype(scales)::value;
             if (wide) attend_kernel<STORE, SCALES, D, true><<<grid, kThreads, 0, s>>>(p, first);

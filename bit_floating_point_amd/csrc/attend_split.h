@@ -20,33 +20,35 @@ inline int64_t most_seen(int64_t length, int64_t window) {
     return window > 0 && window < length - kTilePositions ? window + kTilePositions - 1 : length;
 }
 
-// Parts per sequence: as many as bring the launch to kWantedWorkgroups, none of them shorter than
-// kPartLeast.  Grows with max_length.
+// Parts per sequence, a power of two: as many as bring the launch to kWantedWorkgroups, none of them
+// shorter than kPartLeast.  Grows with max_length.
 inline int32_t split_count(int64_t sequences, int32_t heads, int32_t kv_heads, int64_t max_length, int64_t window) {
     const int64_t tiles = (heads / kv_heads + kHeadTile - 1) / kHeadTile;
     const int64_t units = sequences * kv_heads * tiles;
     const int64_t parts = (most_seen(max_length, window) + kPartLeast - 1) / kPartLeast;
-    int64_t s = (kWantedWorkgroups + units - 1) / units;
-    if (s > parts) s = parts;
-    if (s > kMostSplits) s = kMostSplits;
-    return (int32_t)(s < 1 ? 1 : s);
+    int64_t wanted = (kWantedWorkgroups + units - 1) / units;
+    if (wanted > parts) wanted = parts;
+    int32_t s = 1;
+    while (s < wanted && s < kMostSplits) s *= 2;
+    return s;
 }
 
-// The positions [begin, end) that a sequence of n positions sees are divided from
-// `first` = begin rounded down to a tile, `chunk` at a time; `used` parts have any.
+// The positions [begin, n) that a sequence of n positions sees are divided from `first` = begin
+// rounded down to a tile, `chunk` at a time; `count` of them from there.
 struct SplitRange {
-    int32_t begin, first, chunk, used;
+    int32_t begin, first, count, chunk;
+    FP4_HD int32_t used() const { return count > 0 ? (count - 1) / chunk + 1 : 0; }
+    FP4_HD bool has(int32_t split) const { return (int64_t)split * chunk < count; }
 };
-FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t splits) {
+// (`splits` as its logarithm: workgroups divide by it)
+FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log) {
     SplitRange r;
     r.begin = window > 0 && window < n ? n - window : 0;
     r.first = r.begin / kTilePositions * kTilePositions;
-    const int32_t count = n - r.first;
-    const int32_t step = kTilePositions * kAttendWaves;  // every wavefront gets as many tiles
-    int32_t chunk = (count + splits - 1) / splits;
-    chunk = chunk < kPartLeast ? kPartLeast : (int32_t)(((int64_t)chunk + step - 1) / step * step);
-    r.chunk = chunk;
-    r.used = count > 0 ? (count - 1) / chunk + 1 : 0;
+    r.count = n - r.first;
+    constexpr int32_t step = kTilePositions * kAttendWaves;  // every wavefront gets as many tiles
+    const int32_t chunk = (int32_t)(((int64_t)r.count + (1 << split_log) - 1) >> split_log);
+    r.chunk = chunk < kPartLeast ? kPartLeast : (chunk + step - 1) / step * step;
     return r;
 }
 

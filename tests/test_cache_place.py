@@ -43,13 +43,17 @@ static void places() {
 static void check(int64_t sequences, int32_t heads, int32_t kv_heads, int32_t most, int32_t window, int32_t n, bool each) {
     const int32_t splits = split_count(sequences, heads, kv_heads, most, window);
     need(splits >= 1 && splits <= kMostSplits, "splits", sequences, most, splits);
-    const SplitRange r = split_range(n, window, splits);
+    need((splits & (splits - 1)) == 0, "power of two", sequences, most, splits);
+    const SplitRange r = split_range(n, window, __builtin_ctz(splits));
+    const int32_t parts = r.used();
     const int32_t begin = window > 0 && window < n ? n - window : 0;
     need(r.begin == begin && r.first <= begin && begin - r.first < kTilePositions && r.first % kTilePositions == 0, "begin", n, window, r.first);
     need(r.chunk > 0 && r.chunk % kTilePositions == 0, "chunk", n, splits, r.chunk);
-    need(r.used <= splits && (r.used > 0) == (n > 0), "used", n, splits, r.used);
+    need(parts <= splits && (parts > 0) == (n > 0), "used", n, splits, parts);
+    for (int32_t i = 0; i < splits; i++) need(r.has(i) == (i < parts), "has", n, i, parts);
+    need(r.count == n - r.first && (parts > 1) == (r.count > r.chunk), "count", n, r.count, r.chunk);
     int64_t at = r.first;
-    for (int32_t i = 0; i < r.used; i++) {
+    for (int32_t i = 0; i < parts; i++) {
         const int64_t b = r.first + (int64_t)i * r.chunk;
         const int32_t e = n - (int32_t)b < r.chunk ? n : (int32_t)b + r.chunk;  // the kernel's expression
         need(b == at && e > b && e <= n, "part", n, i, e);
