@@ -9,11 +9,13 @@ element types, shapes and contiguity.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
 from . import _lib as L
-from .layer import _flat, _need, _raw_stream, _type
+from .layer import _TYPES, _flat, _need, _raw_stream
 
 P, I32, I64, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
@@ -24,9 +26,9 @@ class fp4_kv_cache(ctypes.Structure):
                 ("gran", L.fp4_gran), ("k_scales", P), ("v_scales", P)]
 
 
-class fp4_cache_rows(ctypes.Structure):
-    _fields_ = [("page_table", P), ("sequences", I64), ("max_pages", I64), ("ld_table", I64), ("positions", P),
-                ("sequence_of", P)]
+class fp4_cache_rows_desc(ctypes.Structure):
+    _fields_ = [("page_table", P), ("sequences", I64), ("max_pages", I64), ("ld_table", I64), ("tokens", I64), ("positions", P),
+                ("sequence_of", P), ("k", P), ("ldk", I64), ("v", P), ("ldv", I64), ("dtype", I32), ("reserved", I32)]
 
 
 class fp4_attend_desc(ctypes.Structure):
@@ -35,13 +37,26 @@ class fp4_attend_desc(ctypes.Structure):
                 ("y_dtype", I32), ("y", P), ("ldy", I64), ("lse", P)]
 
 
-_CACHE, _ROWS, _ATTEND = (ctypes.POINTER(t) for t in (fp4_kv_cache, fp4_cache_rows, fp4_attend_desc))
+# descriptors of a call go as bytes (see _pack), the cache's as it is kept
+_CACHE, _DESC = ctypes.POINTER(fp4_kv_cache), ctypes.c_char_p
 SIGNATURES = {
-    "fp4_cache_write": (I32, [_CACHE, _ROWS, I64, P, I64, P, I64, I32, P]),
-    "fp4_cache_read": (I32, [_CACHE, _ROWS, I64, P, I64, P, I64, I32, P]),
+    "fp4_cache_write": (I32, [_CACHE, _DESC, P]),
+    "fp4_cache_read": (I32, [_CACHE, _DESC, P]),
     "fp4_attend_workspace_size": (ctypes.c_size_t, [I64, I32, I32, I32, I64, I64]),
-    "fp4_attend": (I32, [_CACHE, _ATTEND, P, ctypes.c_size_t, P]),
+    "fp4_attend": (I32, [_CACHE, _DESC, P, ctypes.c_size_t, P]),
 }
+
+
+def _pack(struct_type):
+    """A function that packs the fields of a descriptor (pointers as numbers, 0 for none) into its bytes: a call on a
+    few tokens takes as long as its marshalling, and a ctypes structure costs four times this."""
+    codes = {P: "P", I64: "q", I32: "i", F32: "f"}
+    s = struct.Struct("@" + "".join(codes[f[1]] for f in struct_type._fields_))
+    assert s.size == ctypes.sizeof(struct_type)
+    return s.pack
+
+
+_rows_desc, _attend_desc = _pack(fp4_cache_rows_desc), _pack(fp4_attend_desc)
 
 _entry = {}
 
@@ -61,16 +76,21 @@ def _call(name):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _launch(dev, func, *args):
-    """A call on a device's current stream, with that device current."""
-    f = _call(func)
-    if dev.index == _current_device() and _raw_stream is not None:
-        status = f(*args, _raw_stream(dev.index))
+def _launch(cache, func, *args):
+    """A call on a cache, on its device's current stream and with that device current."""
+    f = _entry.get(func) or _call(func)
+    if _raw_stream is not None and cache.index == _current_device():
+        status = f(cache.desc, *args, _raw_stream(cache.index))
     else:
-        with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(cache.device):
+            status = f(cache.desc, *args, torch.cuda.current_stream(cache.device).cuda_stream)
     if status:
         L.check(status, func)
+
+
+@functools.lru_cache(4096)
+def _workspace_size(*sizes):
+    return _call("fp4_attend_workspace_size")(*sizes)
 
 
 class KVCache:
@@ -80,7 +100,7 @@ class KVCache:
     a row), in any order of strides that keeps a row contiguous (the same for both).  Codes have scales: with
     g = gran("row") one a row, f32 or f16 [pages, kv_heads, page_size] contiguous; with g = gran("tensor") one
     f32 value each, given.  The object keeps the tensors; make it once and use it for every call."""
-    __slots__ = ("k", "v", "k_scales", "v_scales", "grid", "gran", "head_dim", "kv_heads", "page_size", "device", "desc")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "grid", "gran", "head_dim", "kv_heads", "page_size", "device", "index", "desc")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
                  v_scales: torch.Tensor | None = None, grid: L.fp4_grid | None = None, g: L.fp4_gran | None = None):
@@ -104,7 +124,7 @@ class KVCache:
         strides = [st * k.element_size() if n > 1 else 0 for n, st in zip(k.shape, k.stride())]
         self.k, self.v, self.k_scales, self.v_scales, self.grid, self.gran = k, v, k_scales, v_scales, grid, g
         self.head_dim = width * (2 if grid is not None and (grid.e, grid.m) == (2, 1) else 1)
-        self.kv_heads, self.page_size, self.device = heads, size, dev
+        self.kv_heads, self.page_size, self.device, self.index = heads, size, dev, k.get_device()
         self.desc = fp4_kv_cache(
             k.data_ptr(), v.data_ptr(), pages, *strides[:3], heads, size, self.head_dim, L.FP4_BF16 if grid is None else L.FP4_PACKED,
             grid if grid is not None else L.fp4_grid(), g, k_scales.data_ptr() if k_scales is not None else None,
@@ -130,33 +150,57 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, grid: L.f
     return KVCache(torch.zeros(shape, dtype=kind, device=device), torch.zeros(shape, dtype=kind, device=device), k_scale, v_scale, grid, g)
 
 
-# The checks below run on every call, beside kernels of a few microseconds.
-def _heads(t, name, rows, heads, dim, dev):
-    """Leading dimension of rows of heads: [rows, heads, dim], the heads of a row side by side."""
-    if t.shape != (rows, heads, dim) or t.device != dev:
-        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}] on {dev}, not {list(t.shape)} on {t.device}")
+# The checks below run on every call, beside kernels of a few microseconds: one condition each, the message
+# made only when it fails.  (Devices are compared by their number, -1 for none.)
+def _heads(t, name, shape, cache):
+    """Leading dimension of rows of heads [rows, heads, dim], the heads of a row side by side."""
+    if t.shape != shape or t.get_device() != cache.index:
+        raise ValueError(f"{name} must be {list(shape)} on {cache.device}, not {list(t.shape)} on {t.device}")
     ld, head, step = t.stride()
+    rows, heads, dim = shape
     if step != 1 or (head != dim and heads > 1):
         raise ValueError(f"the heads of {name} must lie side by side")
     return ld if rows > 1 or ld > heads * dim else heads * dim
 
 
-def _table(t, dev):
+def _table(t, cache):
     """Sizes of a page table: rows, columns, leading dimension."""
-    if t.dim() != 2 or t.dtype != torch.int32 or t.device != dev or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"page_table must be int32 [sequences, pages] on {dev}, row-major")
-    rows, cols = t.shape
-    return rows, cols, (t.stride(0) if rows > 1 or t.stride(0) > cols else cols)
+    shape = t.shape
+    if len(shape) != 2 or t.dtype != torch.int32 or t.get_device() != cache.index:
+        raise ValueError(f"page_table must be int32 [sequences, pages] on {cache.device}")
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("page_table must be row-major")
+    return rows, cols, (ld if rows > 1 or ld > cols else cols)
 
 
-def _rows(cache, page_table, positions, sequences):
-    dev = cache.device
-    if positions.dim() != 1:
-        raise ValueError("positions must be one list")
-    n = positions.shape[0]
-    rows, cols, ld = _table(page_table, dev)
-    return n, fp4_cache_rows(page_table.data_ptr(), rows, cols, ld, _flat(positions, "positions", n, torch.int32, dev),
-                             _flat(sequences, "sequences", n, torch.int32, dev))
+def _list(t, name, count, dtype, cache):
+    """Pointer of a contiguous tensor of `count` values (None: 0)."""
+    if t is None:
+        return 0
+    if t.numel() != count or t.dtype != dtype or t.get_device() != cache.index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} values on {cache.device}")
+    return t.data_ptr()
+
+
+def _float(t, name):
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _rows_call(func, k, v, cache, page_table, positions, sequences):
+    n = positions.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
+    kind = _float(k, "k")
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have one dtype")
+    _launch(cache, func, _rows_desc(
+        page_table.data_ptr(), *_table(page_table, cache), n, _list(positions, "positions", n, torch.int32, cache),
+        _list(sequences, "sequences", n, torch.int32, cache), k.data_ptr(), _heads(k, "k", shape, cache), v.data_ptr(),
+        _heads(v, "v", shape, cache), kind, 0))
 
 
 def fp4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, positions: torch.Tensor,
@@ -166,28 +210,19 @@ def fp4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table
     Token i becomes position positions[i] (int32) of sequence sequences[i] (int32; i itself without them), in page
     page_table[sequence, position // page_size] (int32 [sequences, pages]).  Tokens whose position is negative or past
     the table, or whose page is not in the cache, are skipped (padding).  No two tokens may have one place."""
-    n, rows = _rows(cache, page_table, positions, sequences)
-    heads, dim, dev = cache.kv_heads, cache.head_dim, cache.device
-    if k.dtype != v.dtype:
-        raise ValueError("k and v must have one dtype")
-    _launch(dev, "fp4_cache_write", cache.desc, rows, n, k.data_ptr(), _heads(k, "k", n, heads, dim, dev), v.data_ptr(),
-            _heads(v, "v", n, heads, dim, dev), _type(k, "k"))
+    _rows_call("fp4_cache_write", k, v, cache, page_table, positions, sequences)
 
 
 def fp4_cache_read(cache: KVCache, page_table: torch.Tensor, positions: torch.Tensor, sequences: torch.Tensor | None = None,
                    dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
     """The keys and values that the cache holds for tokens given as in fp4_cache_write, as (k, v)
     [tokens, kv_heads, head_dim]; zeros for tokens without a place."""
-    n, rows = _rows(cache, page_table, positions, sequences)
-    heads, dim, dev = cache.kv_heads, cache.head_dim, cache.device
+    shape = (positions.numel(), cache.kv_heads, cache.head_dim)
     if k is None:
-        k = torch.empty((n, heads, dim), dtype=dtype if v is None else v.dtype, device=dev)
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device)
     if v is None:
-        v = torch.empty((n, heads, dim), dtype=k.dtype, device=dev)
-    if k.dtype != v.dtype:
-        raise ValueError("k and v must have one dtype")
-    _launch(dev, "fp4_cache_read", cache.desc, rows, n, k.data_ptr(), _heads(k, "k", n, heads, dim, dev), v.data_ptr(),
-            _heads(v, "v", n, heads, dim, dev), _type(k, "k"))
+        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    _rows_call("fp4_cache_read", k, v, cache, page_table, positions, sequences)
     return k, v
 
 
@@ -203,26 +238,27 @@ def fp4_attend(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, length
     table's, unless given: a smaller one saves launching parts that have no positions).  Returns y of q's shape (q's dtype
     unless y or y_dtype is given); a sequence that sees nothing has zeros.  lse (f32 [sequences, heads]) takes the logarithms of
     the sums of exponentials.  A drafted token is a sequence of its own with the same row of the table."""
-    _need(q.dim() == 3, "q must be [sequences, heads, head_dim]")
-    (n, heads, dim), dev = q.shape, cache.device
-    _need(dim == cache.head_dim, "q must have the cache's head_dim")
+    shape, dim = q.shape, cache.head_dim
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"q must be [sequences, heads, {dim}]")
+    n, heads, _ = shape
     if y is None:
-        y = torch.empty((n, heads, dim), dtype=y_dtype or q.dtype, device=dev)
-    rows, cols, ld = _table(page_table, dev)
+        y = torch.empty(shape, dtype=y_dtype or q.dtype, device=cache.device)
+    rows, cols, ld = _table(page_table, cache)
     if rows != n:
         raise ValueError(f"page_table must have a row for each of {n} sequences")
     most = cols * cache.page_size
     if max_length is not None and max_length < most:
         most = max_length
-    need = _call("fp4_attend_workspace_size")(n, heads, cache.kv_heads, dim, most, window)
+    need, at = _workspace_size(n, heads, cache.kv_heads, dim, most, window), None
     if need:
-        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-            raise ValueError(f"workspace must be contiguous memory on {dev}")
+        if workspace is not None and (workspace.get_device() != cache.index or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous memory on {cache.device}")
         if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    d = fp4_attend_desc(
-        n, heads, _type(q, "q"), q.data_ptr(), _heads(q, "q", n, heads, dim, dev), page_table.data_ptr(), cols, ld,
-        _flat(lengths, "lengths", n, torch.int32, dev), most, window, dim ** -0.5 if scale is None else scale, _type(y, "y"),
-        y.data_ptr(), _heads(y, "y", n, heads, dim, dev), _flat(lse, "lse", n * heads, torch.float32, dev))
-    _launch(dev, "fp4_attend", cache.desc, d, workspace.data_ptr() if need else None, need)
+            workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        at = workspace.data_ptr()
+    _launch(cache, "fp4_attend", _attend_desc(
+        n, heads, _float(q, "q"), q.data_ptr(), _heads(q, "q", shape, cache), page_table.data_ptr(), cols, ld,
+        _list(lengths, "lengths", n, torch.int32, cache), most, window, dim ** -0.5 if scale is None else scale, _float(y, "y"),
+        y.data_ptr(), _heads(y, "y", shape, cache), _list(lse, "lse", n * heads, torch.float32, cache)), at, need)
     return y

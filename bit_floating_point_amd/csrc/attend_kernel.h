@@ -248,27 +248,28 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
         v_all = *reinterpret_cast<const float*>(c.v_scales);
     }
 
-    // q of head n, in K's order of columns
+    // q of head n, in K's order of columns: loaded here, in terms once the first tile is on its way
     bf16x8 q[kQTerms][L::kSteps];
+    Raw8 q_raw[WIDE ? L::kSteps : 1];
+    const bool q_bf16 = !WIDE || p.q_bf16;
     {
-        const bool there = n < heads;
         const int64_t row = sequence * p.ldq + (first_head + n) * D;
-        repeat<L::kLoads>([&](auto l) {
-            constexpr int first = L::k_first(l), steps = L::k_steps(l);
+        repeat<L::kLoads>([&](auto x) {
+            constexpr int first = L::k_first(x), steps = L::k_steps(x);
 #pragma unroll
             for (int i = 0; i < steps; i++) {
                 const int64_t col = row + first * 32 + g * 8 * steps + 8 * i;
-                if constexpr (WIDE) {
-                    float x[8] = {};
-                    if (there) get8(p.q, p.q_bf16, col, x);
-                    bf16x8 t[kQTerms];
-                    terms_of<kQTerms>(x, t);
-#pragma unroll
-                    for (int k = 0; k < kQTerms; k++) q[k][first + i] = t[k];
-                } else {
-                    q[0][first + i] = bf16x8{};
-                    if (there) q[0][first + i] = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const uint16_t*>(p.q) + col);
+                uint4 a{}, b{};
+                if (n < heads) {
+                    if (q_bf16) {
+                        a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + col);
+                    } else {
+                        a = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p.q) + col)[0];
+                        b = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p.q) + col)[1];
+                    }
                 }
+                if constexpr (WIDE) q_raw[first + i] = Raw8{a, b};
+                else q[0][first + i] = __builtin_bit_cast(bf16x8, a);
             }
         });
     }
@@ -448,9 +449,18 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
         load_values(tile);
         // q is waited for here, beside those: in the loop it would be waited for, with all loads, in every turn
 #pragma unroll
-        for (int k = 0; k < kQTerms; k++)
+        for (int s = 0; s < L::kSteps; s++) {
+            if constexpr (WIDE) {
+                float x[8];
+                if (q_bf16) raw8_to_float<true>(q_raw[s], x);
+                else raw8_to_float<false>(q_raw[s], x);
+                bf16x8 t[kQTerms];
+                terms_of<kQTerms>(x, t);
 #pragma unroll
-            for (int s = 0; s < L::kSteps; s++) arrived(q[k][s]);
+                for (int k = 0; k < kQTerms; k++) q[k][s] = t[k];
+            }
+            arrived(q[0][s]);
+        }
         for (int i = 0; i + 1 < count; i++) step(i, std::true_type{});
         step(count - 1, std::false_type{});
     }

@@ -120,31 +120,31 @@ fp4_status table_of(const int32_t* table, int64_t sequences, int64_t max_pages, 
     return FP4_OK;
 }
 
-// what a call on rows of tokens launches with; p->tokens 0: nothing to do
-fp4_status rows_of(const fp4_kv_cache* cache, const fp4_cache_rows* rows, int64_t tokens, const void* k, int64_t ldk, const void* v,
-                   int64_t ldv, int32_t dtype, CacheRowsParams* p) {
+// what a call on rows of tokens launches with
+fp4_status rows_of(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, CacheRowsParams* p) {
     fp4_status st = cache_of(cache, &p->c);
     if (st) return st;
-    if (!rows) return report(FP4_ERR_INVALID_ARG, "null descriptor");
-    if (tokens < 0) return report(FP4_ERR_INVALID_ARG, "bad sizes tokens=%lld", (long long)tokens);
-    if (!float_type(dtype)) return report(FP4_ERR_INVALID_ARG, "dtype must be FP4_F32 or FP4_BF16");
-    if ((st = table_of(rows->page_table, rows->sequences, rows->max_pages, rows->ld_table, p->c, &p->capacity))) return st;
+    if (!d) return report(FP4_ERR_INVALID_ARG, "null descriptor");
+    if (d->reserved != 0) return report(FP4_ERR_INVALID_ARG, "reserved must be 0");
+    if (d->tokens < 0) return report(FP4_ERR_INVALID_ARG, "bad sizes tokens=%lld", (long long)d->tokens);
+    if (!float_type(d->dtype)) return report(FP4_ERR_INVALID_ARG, "dtype must be FP4_F32 or FP4_BF16");
+    if ((st = table_of(d->page_table, d->sequences, d->max_pages, d->ld_table, p->c, &p->capacity))) return st;
     const int64_t cols = (int64_t)p->c.kv_heads * p->c.head_dim;
-    if ((st = matrix("k", k, tokens, ldk, cols, dtype)) || (st = matrix("v", v, tokens, ldv, cols, dtype))) return st;
-    if (tokens > 0 && (!k || !v || !rows->positions)) return report(FP4_ERR_INVALID_ARG, "null pointer");
-    if (!aligned(rows->positions, 4) || !aligned(rows->sequence_of, 4))
+    if ((st = matrix("k", d->k, d->tokens, d->ldk, cols, d->dtype)) || (st = matrix("v", d->v, d->tokens, d->ldv, cols, d->dtype))) return st;
+    if (d->tokens > 0 && (!d->k || !d->v || !d->positions)) return report(FP4_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(d->positions, 4) || !aligned(d->sequence_of, 4))
         return report(FP4_ERR_ALIGNMENT, "positions and sequence_of must be 4-byte aligned");
-    p->table = rows->page_table;
-    p->sequences = rows->sequences;
-    p->ld_table = rows->ld_table;
-    p->positions = rows->positions;
-    p->sequence_of = rows->sequence_of;
-    p->tokens = tokens;
-    p->k_rows = const_cast<void*>(k);
-    p->v_rows = const_cast<void*>(v);
-    p->ldk = ldk;
-    p->ldv = ldv;
-    p->bf16 = dtype == FP4_BF16;
+    p->table = d->page_table;
+    p->sequences = d->sequences;
+    p->ld_table = d->ld_table;
+    p->positions = d->positions;
+    p->sequence_of = d->sequence_of;
+    p->tokens = d->tokens;
+    p->k_rows = d->k;
+    p->v_rows = d->v;
+    p->ldk = d->ldk;
+    p->ldv = d->ldv;
+    p->bf16 = d->dtype == FP4_BF16;
     return FP4_OK;
 }
 
@@ -159,22 +159,20 @@ int64_t capped(int64_t length) { return length < kMostPositions ? length : kMost
 
 extern "C" {
 
-fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows* rows, int64_t tokens, const void* k, int64_t ldk,
-                           const void* v, int64_t ldv, int32_t dtype, void* stream) {
+fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream) {
     CacheRowsParams p{};
-    const fp4_status st = rows_of(cache, rows, tokens, k, ldk, v, ldv, dtype, &p);
+    const fp4_status st = rows_of(cache, d, &p);
     if (st) return st;
-    if (tokens == 0 || rows->sequences == 0 || rows->max_pages == 0) return report_ok();  // no token has a row
+    if (p.tokens == 0 || p.sequences == 0 || p.capacity == 0) return report_ok();  // no token has a row
     return report_hip(launch_cache_write(p, (hipStream_t)stream), "fp4_cache_write");
 }
 
-fp4_status fp4_cache_read(const fp4_kv_cache* cache, const fp4_cache_rows* rows, int64_t tokens, void* k, int64_t ldk, void* v,
-                          int64_t ldv, int32_t dtype, void* stream) {
+fp4_status fp4_cache_read(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream) {
     CacheRowsParams p{};
-    const fp4_status st = rows_of(cache, rows, tokens, k, ldk, v, ldv, dtype, &p);
+    const fp4_status st = rows_of(cache, d, &p);
     if (st) return st;
-    if (tokens == 0) return report_ok();
-    if (k == v) return report(FP4_ERR_INVALID_ARG, "k and v are the same rows");
+    if (p.tokens == 0) return report_ok();
+    if (p.k_rows == p.v_rows) return report(FP4_ERR_INVALID_ARG, "k and v are the same rows");
     return report_hip(launch_cache_read(p, (hipStream_t)stream), "fp4_cache_read");
 }
 

@@ -42,8 +42,8 @@ typedef struct {
     void* v_scales;             /*   contiguous; TENSOR: f32, one value; else NULL     */
 } fp4_kv_cache;
 
-/* Which rows tokens have.  Token i is position positions[i] of sequence sequence_of[i] (or of
- * sequence i), that is slot positions[i] % page_size of page
+/* Rows of tokens.  Token i is position positions[i] of sequence sequence_of[i] (or of sequence i),
+ * that is slot positions[i] % page_size of page
  *   page_table[sequence * ld_table + positions[i] / page_size].
  * A token has no row if its position is negative or past max_pages * page_size, its sequence
  * outside [0, sequences) or its page outside [0, pages). */
@@ -52,27 +52,29 @@ typedef struct {
     int64_t sequences;
     int64_t max_pages;          /* max_pages * page_size <= 2^30                       */
     int64_t ld_table;           /* elements; 0: all sequences have one row             */
+    int64_t tokens;
     const int32_t* positions;   /* int32 [tokens]                                      */
     const int32_t* sequence_of; /* int32 [tokens], or NULL: token i is of sequence i   */
-} fp4_cache_rows;
+    void* k;                    /* [tokens, kv_heads * head_dim], leading dim ldk:     */
+    int64_t ldk;                /*   inputs of a write, outputs of a read              */
+    void* v;                    /* likewise, leading dim ldv                           */
+    int64_t ldv;
+    int32_t dtype;              /* of k and v: FP4_F32 or FP4_BF16                     */
+    int32_t reserved;           /* must be 0                                           */
+} fp4_cache_rows_desc;
 
 /* ---- rows into the cache --------------------------------------------------------- */
-/* The keys and values of `tokens` tokens, k and v [tokens, kv_heads * head_dim], into their
- * rows.  Codes: per row s = fl32(amax / Qmax), no less than 2^-126 unless amax is 0 (f16 scales:
- * rounded to binary16, at most its largest number), or the given s; codes of
- * fl32(x * fl32(1/s)) as fp4_quantize_pack.  bf16: rounded to nearest.  Tokens without a row are
- * skipped; all other rows of the cache stay as they are.  No two tokens of a call may have one
- * row: what it holds then is a mixture of theirs. */
-fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows* rows, int64_t tokens,
-                           const void* k, int64_t ldk, const void* v, int64_t ldv, int32_t dtype,
-                           void* stream);
+/* The keys and values of the tokens into their rows.  Codes: per row s = fl32(amax / Qmax), no
+ * less than 2^-126 unless amax is 0 (f16 scales: rounded to binary16, at most its largest
+ * number), or the given s; codes of fl32(x * fl32(1/s)) as fp4_quantize_pack.  bf16: rounded to
+ * nearest.  Tokens without a row are skipped; all other rows of the cache stay as they are.  No
+ * two tokens of a call may have one row: what it holds then is a mixture of theirs. */
+fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream);
 
 /* ---- rows out of the cache ------------------------------------------------------- */
-/* The values that the rows of `tokens` tokens hold (code value * scale, one rounding to
- * binary32, one to `dtype`), into k and v [tokens, kv_heads * head_dim]; zeros for tokens
- * without a row. */
-fp4_status fp4_cache_read(const fp4_kv_cache* cache, const fp4_cache_rows* rows, int64_t tokens,
-                          void* k, int64_t ldk, void* v, int64_t ldv, int32_t dtype, void* stream);
+/* The values that the tokens' rows hold (code value * scale, one rounding to binary32, one to
+ * `dtype`) into k and v; zeros for tokens without a row. */
+fp4_status fp4_cache_read(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream);
 
 /* ---- attention of one new token per sequence -------------------------------------- */
 typedef struct {

@@ -37,15 +37,21 @@ def cache(**kw):
     return c
 
 
+def call(name, c, d, *more):
+    """A descriptor as the library's C callers give it."""
+    return C._call(name)(c, None if d is None else bytes(d), *more)
+
+
 def rows(**kw):
-    r = C.fp4_cache_rows(page_table=FAKE, sequences=3, max_pages=2, ld_table=2, positions=FAKE, sequence_of=None)
+    r = C.fp4_cache_rows_desc(page_table=FAKE, sequences=3, max_pages=2, ld_table=2, tokens=5, positions=FAKE, sequence_of=None, k=FAKE,
+                              ldk=256, v=OTHER, ldv=256, dtype=L.FP4_BF16)
     for k, v in kw.items():
         setattr(r, k, v)
     return r
 
 
-def move(name, c=None, r=None, tokens=5, k=FAKE, ldk=256, v=OTHER, ldv=256, dtype=L.FP4_BF16):
-    return C._call(name)(c or cache(), r or rows(), tokens, k, ldk, v, ldv, dtype, None)
+def move(name, c=None, **kw):
+    return call(name, c or cache(), rows(**kw), None)
 
 
 def attend(c=None, ws=FAKE, ws_bytes=1 << 30, **kw):
@@ -53,7 +59,7 @@ def attend(c=None, ws=FAKE, ws_bytes=1 << 30, **kw):
                           lengths=FAKE, max_length=32, window=0, scale=1.0, y_dtype=L.FP4_BF16, y=OTHER, ldy=512, lse=None)
     for k, v in kw.items():
         setattr(d, k, v)
-    return C._call("fp4_attend")(c or cache(), d, ws, ws_bytes, None)
+    return call("fp4_attend", c or cache(), d, ws, ws_bytes, None)
 
 
 def test_exports_and_signatures():
@@ -65,7 +71,7 @@ def test_exports_and_signatures():
         assert hasattr(lib, n), n
 
 
-@pytest.mark.parametrize("struct", [C.fp4_kv_cache, C.fp4_cache_rows, C.fp4_attend_desc])
+@pytest.mark.parametrize("struct", [C.fp4_kv_cache, C.fp4_cache_rows_desc, C.fp4_attend_desc])
 def test_struct_layouts(struct, tmp_path):
     fields = [f[0] for f in struct._fields_]
     src = tmp_path / "s.c"
@@ -114,12 +120,12 @@ def test_good_caches(kw):
 
 @pytest.mark.parametrize("status,kw", [
     (INVALID, dict(tokens=-1)), (INVALID, dict(k=None)), (INVALID, dict(v=None)), (INVALID, dict(ldk=255)), (INVALID, dict(ldv=128)),
-    (INVALID, dict(dtype=L.FP4_F16)), (INVALID, dict(r=rows(page_table=None))), (INVALID, dict(r=rows(positions=None))),
-    (INVALID, dict(r=rows(sequences=-1))), (INVALID, dict(r=rows(sequences=1 << 31))), (INVALID, dict(r=rows(max_pages=-1))),
-    (INVALID, dict(r=rows(ld_table=1))), (UNSUPPORTED, dict(r=rows(max_pages=(1 << 26) + 1, ld_table=1 << 27))),
-    (UNSUPPORTED, dict(r=rows(ld_table=1 << 60))), (UNSUPPORTED, dict(tokens=1 << 40, ldk=1 << 40)),
-    (ALIGNMENT, dict(k=ODD)), (ALIGNMENT, dict(v=ODD)), (ALIGNMENT, dict(ldk=260)), (ALIGNMENT, dict(r=rows(page_table=0x10002))),
-    (ALIGNMENT, dict(r=rows(positions=0x10002))), (ALIGNMENT, dict(r=rows(sequence_of=0x10001)))])
+    (INVALID, dict(dtype=L.FP4_F16)), (INVALID, dict(reserved=1)), (INVALID, dict(page_table=None)), (INVALID, dict(positions=None)),
+    (INVALID, dict(sequences=-1)), (INVALID, dict(sequences=1 << 31)), (INVALID, dict(max_pages=-1)),
+    (INVALID, dict(ld_table=1)), (UNSUPPORTED, dict(max_pages=(1 << 26) + 1, ld_table=1 << 27)),
+    (UNSUPPORTED, dict(ld_table=1 << 60)), (UNSUPPORTED, dict(tokens=1 << 40, ldk=1 << 40)),
+    (ALIGNMENT, dict(k=ODD)), (ALIGNMENT, dict(v=ODD)), (ALIGNMENT, dict(ldk=260)), (ALIGNMENT, dict(page_table=0x10002)),
+    (ALIGNMENT, dict(positions=0x10002)), (ALIGNMENT, dict(sequence_of=0x10001))])
 def test_bad_rows(status, kw):
     for name in ("fp4_cache_write", "fp4_cache_read"):
         assert move(name, **kw) == status, L.lib().fp4_last_error()
@@ -128,11 +134,11 @@ def test_bad_rows(status, kw):
 def test_rows_that_nobody_has():
     """No tokens: nothing to do.  No sequences or no pages: nothing to write."""
     for name in ("fp4_cache_write", "fp4_cache_read"):
-        assert move(name, tokens=0, k=None, v=None, r=rows(positions=None)) == OK
-        assert C._call(name)(None, rows(), 1, FAKE, 256, OTHER, 256, 0, None) == INVALID
-        assert C._call(name)(cache(), None, 1, FAKE, 256, OTHER, 256, 0, None) == INVALID
-    assert move("fp4_cache_write", r=rows(sequences=0, page_table=None)) == OK
-    assert move("fp4_cache_write", r=rows(max_pages=0, page_table=None)) == OK
+        assert move(name, tokens=0, k=None, v=None, positions=None) == OK
+        assert call(name, None, rows(), None) == INVALID
+        assert call(name, cache(), None, None) == INVALID
+    assert move("fp4_cache_write", sequences=0, page_table=None) == OK
+    assert move("fp4_cache_write", max_pages=0, page_table=None) == OK
     assert move("fp4_cache_read", v=FAKE) == INVALID
 
 
@@ -152,8 +158,8 @@ def test_bad_attend(status, kw):
 
 def test_attend_of_no_sequences():
     assert attend(sequences=0, q=None, y=None, lengths=None, page_table=None) == OK
-    assert C._call("fp4_attend")(None, C.fp4_attend_desc(), None, 0, None) == INVALID
-    assert C._call("fp4_attend")(cache(), None, None, 0, None) == INVALID
+    assert call("fp4_attend", None, C.fp4_attend_desc(), None, 0, None) == INVALID
+    assert call("fp4_attend", cache(), None, None, 0, None) == INVALID
 
 
 def test_workspace_size():
