@@ -97,9 +97,10 @@ __device__ __forceinline__ void load_bytes(__amdgpu_buffer_rsrc_t r, uint32_t of
         w[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, more, kOnce);
     }
 }
-// the buffer from `base` on: pages and scales are addressed by their own starts, offsets stay below 2^31
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t off) {
-    return buf_make(reinterpret_cast<const uint8_t*>(base) + off, 0x7fffffff);
+// The buffer from `base` + off on: pages and scales are addressed by their own starts, offsets stay below
+// 2^31.  With `there` false it is empty: loads give zeros and read nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t off, bool there) {
+    return buf_make(reinterpret_cast<const uint8_t*>(base) + off, there ? 0x7fffffff : 0);
 }
 
 __device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
@@ -193,8 +194,8 @@ struct RowScales {
     static constexpr int kBytes = SCALES == kScaleRowF32 ? 4 : SCALES == kScaleRowF16 ? 2 : 0;
     uint32_t w[2][4];
     // `first`: index of the half's first scale
-    __device__ __forceinline__ void load(const void* scales, int64_t first, int half, int g) {
-        if constexpr (kBytes) load_bytes<4 * kBytes>(buffer_at(scales, first * kBytes), (uint32_t)(4 * g * kBytes), 0, w[half]);
+    __device__ __forceinline__ void load(const void* scales, int64_t first, int half, int g, bool there) {
+        if constexpr (kBytes) load_bytes<4 * kBytes>(buffer_at(scales, first * kBytes, there), (uint32_t)(4 * g * kBytes), 0, w[half]);
     }
     // x * (row j's scale) + y, rounded once: one instruction, binary16 scales are converted inside it
     __device__ __forceinline__ float fma(int j, float x, float y) const {
@@ -218,17 +219,20 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     using L = Plan<STORE, D>;
     constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
     constexpr int kRound = 8;  // heads whose parts are joined at a time
+    constexpr int H = 2, J = 4 * H;  // halves of a tile, a lane's positions in it
     __shared__ float joined[kAttendWaves][kRound][D + 4];
     __shared__ float2 stats[kAttendWaves][kHeadTile];
 
     const CacheParams& c = p.c;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // workgroup (part, kv head and tile of its query heads, sequence)
+    // Workgroup (kv head and tile of its query heads, sequence, part).  Workgroups go to the eight XCDs in turn:
+    // with parts first, those that most sequences do not have would leave the same XCDs idle (33
+    // sequences of 1000 positions: 17 against 9 us).
     const uint32_t tiles = (uint32_t)(p.share + kHeadTile - 1) / kHeadTile;
-    const int split = (int)blockIdx.x, kv_head = (int)(tiles == 1 ? blockIdx.y : blockIdx.y / tiles);
-    const int head_tile = (int)(blockIdx.y - (uint32_t)kv_head * tiles);
-    const int64_t sequence = first_sequence + blockIdx.z;
+    const int split = (int)blockIdx.z, kv_head = (int)(tiles == 1 ? blockIdx.x : blockIdx.x / tiles);
+    const int head_tile = (int)(blockIdx.x - (uint32_t)kv_head * tiles);
+    const int64_t sequence = first_sequence + blockIdx.y;
     const int heads = min(p.share - head_tile * kHeadTile, kHeadTile);  // of this tile
     const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeadTile;
 
@@ -279,18 +283,18 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     f32x4 acc[L::kCols];
     repeat<L::kCols>([&](auto j) { acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
 
-    uint32_t kw[2][L::kWords], vw[8][L::vWords];
+    uint32_t kw[H][L::kWords], vw[J][L::vWords];  // the tile on its way
     RowScales<SCALES> ks, vs;
 
-    // Where the halves of 32 of this wavefront's tiles lie, one half a lane: the byte offset of the first
-    // of the 16 rows and the index of its scale.  A half that is not in the cache or has nothing
+    // Where the halves of the next 64 / H of this wavefront's tiles lie, one half a lane: the byte offset of
+    // the first of the 16 rows and the index of its scale.  A half that is not in the cache or has nothing
     // to be seen: page 0 in its place, read and not used, and the highest bit set.
     const int32_t* table = p.table + sequence * p.ld_table;
     const int slots = (1 << c.page_log) - 1;
     constexpr uint32_t kAbsent = 0x80000000u;
     uint32_t row_low = 0, row_high = 0, scale_low = 0, scale_high = 0;
     auto find_pages = [&](int i) {
-        const int t = begin + ((i + (lane >> 1)) * kAttendWaves + wave) * kTilePositions + 16 * (lane & 1);
+        const int t = begin + ((i + lane / H) * kAttendWaves + wave) * kTilePositions + 16 * (lane % H);
         const int found = t < end ? page_at(table + (t >> c.page_log), c.pages) : -1, page = max(found, 0);
         const int64_t row = page * c.stride_page + kv_head * c.stride_head + (int64_t)(t & slots) * c.stride_row;
         row_low = (uint32_t)row;
@@ -304,15 +308,17 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     // a tile of this wavefront: its first position, and where its halves lie
     struct Tile {
         int t;
-        uint32_t high[2];  // kAbsent
-        int64_t row[2], scale[2];
+        bool there;        // else past the last one, and nothing is loaded
+        uint32_t high[H];  // kAbsent
+        int64_t row[H], scale[H];
     };
     auto tile_of = [&](int i) {
         Tile r;
         r.t = begin + (i * kAttendWaves + wave) * kTilePositions;
+        r.there = i < count;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int from = 2 * (i & 31) + h;
+        for (int h = 0; h < H; h++) {
+            const int from = H * (i & (64 / H - 1)) + h;
             r.high[h] = __builtin_amdgcn_readlane(row_high, from);
             r.row[h] = (int64_t)(((uint64_t)(r.high[h] & ~kAbsent) << 32) | (uint32_t)__builtin_amdgcn_readlane(row_low, from));
             if constexpr (kRows)
@@ -324,19 +330,19 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     const uint32_t key_row = (uint32_t)n * c.stride_row, value_row = (uint32_t)(4 * g) * c.stride_row;
     auto load_keys = [&](const Tile& tile) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const auto rows = buffer_at(c.k, tile.row[h]);
+        for (int h = 0; h < H; h++) {
+            const auto rows = buffer_at(c.k, tile.row[h], tile.there);
             repeat<L::kLoads>([&](auto x) {
                 constexpr int first = L::k_first(x), steps = L::k_steps(x), bytes = steps * L::kStepBytes;
                 load_bytes<bytes>(rows, key_row + (uint32_t)(first * 4 * L::kStepBytes + g * bytes), 0, kw[h] + first * L::kStepBytes / 4);
             });
-            ks.load(c.k_scales, tile.scale[h], h, g);
+            ks.load(c.k_scales, tile.scale[h], h, g, tile.there);
         }
     };
     auto load_values = [&](const Tile& tile) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const auto rows = buffer_at(c.v, tile.row[h]);
+        for (int h = 0; h < H; h++) {
+            const auto rows = buffer_at(c.v, tile.row[h], tile.there);
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 repeat<L::vLoads>([&](auto x) {
@@ -344,53 +350,55 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
                     load_bytes<bytes>(rows, value_row + (uint32_t)(first * 2 * L::kBits + n * bytes), (uint32_t)j * c.stride_row,
                                       vw[4 * h + j] + word);
                 });
-            vs.load(c.v_scales, tile.scale[h], h, g);
+            vs.load(c.v_scales, tile.scale[h], h, g, tile.there);
         }
     };
 
-    Tile tile{};
-    // Tile i.  `more`: the loads of tile i + 1 start where the registers of i's keys and then of its values
-    // are free.  (The last tile is a copy of its own: a load under a condition would be waited for
-    // where the condition ends.)
-    auto step = [&](int i, auto more) {
-        // Z^T of both halves
-        f32x4 z2[2];
+    Tile tile;
+    // Tile i.  The loads of tile i + 1 start where the registers of i's keys and then of its values are free.
+    // (Past the last tile they are of empty buffers: loads under a condition would be waited for where the
+    // condition ends.)
+    auto step = [&](int i) {
+        // Z^T of every half
+        f32x4 z[H];
 #pragma unroll
-        for (int h = 0; h < 2; h++) z2[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int h = 0; h < H; h++) z[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < L::kSteps; s++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < H; h++) {
                 const bf16x8 a = key_operand<STORE>(kw[h] + s * L::kStepBytes / 4);
 #pragma unroll
-                for (int k = kQTerms - 1; k >= 0; k--) z2[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z2[h], 0, 0, 0);
+                for (int k = kQTerms - 1; k >= 0; k--) z[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z[h], 0, 0, 0);
             }
         // x = z - m
-        float x[8];
+        float x[J];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float dot = z2[j / 4][j % 4];
+        for (int j = 0; j < J; j++) {
+            const float dot = z[j / 4][j % 4];
             if constexpr (kRows) x[j] = ks.fma(j, dot * factor, -m);
             else x[j] = __builtin_fmaf(dot, factor, -m);
         }
-        Tile next{};
-        if constexpr (more) {
-            if (((i + 1) & 31) == 0) find_pages(i + 1);
-            next = tile_of(i + 1);
-            load_keys(next);
-        }
+        if (((i + 1) & (64 / H - 1)) == 0) find_pages(i + 1);
+        const Tile next = tile_of(i + 1);
+        load_keys(next);
         // What is not seen has no weight, whatever its rows and scales hold.  (It may call for a new
         // reference in vain.)
-        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && (int)(tile.high[0] | tile.high[1]) >= 0;
+        uint32_t absent = 0;
+        float most = x[0];
+#pragma unroll
+        for (int h = 0; h < H; h++) absent |= tile.high[h];
+#pragma unroll
+        for (int j = 1; j < J; j++) most = fmaxf(most, x[j]);
+        const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && (absent & kAbsent) == 0;
         auto seen = [&](int j) {
             const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
-            return whole | ((t >= range.begin) & (t < end) & ((int)tile.high[j / 4] >= 0));
+            return whole | ((t >= range.begin) & (t < end) & ((tile.high[j / 4] & kAbsent) == 0));
         };
-        const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
         if (fresh | __any(most > kSlack)) {
             float top = kNothing;
 #pragma unroll
-            for (int j = 0; j < 8; j++) top = fmaxf(top, seen(j) ? x[j] : kNothing);
+            for (int j = 0; j < J; j++) top = fmaxf(top, seen(j) ? x[j] : kNothing);
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             // m moves to the first tile's largest z that has any (it was 0 until then), then upwards
@@ -402,22 +410,22 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
             l *= f;
             repeat<L::kCols>([&](auto j) { acc[j] *= f; });
 #pragma unroll
-            for (int j = 0; j < 8; j++) x[j] -= top;
+            for (int j = 0; j < J; j++) x[j] -= top;
         }
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = power2(x[j]);
+        for (int j = 0; j < J; j++) x[j] = power2(x[j]);
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) x[j] = seen(j) ? x[j] : 0.0f;
+            for (int j = 0; j < J; j++) x[j] = seen(j) ? x[j] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+        for (int j = 0; j < J; j++) {
             l += x[j];
             if constexpr (kRows) x[j] = vs.fma(j, x[j], 0.0f);
         }
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < J; j++) {
                 if constexpr (kRows) x[j] = seen(j) ? x[j] : 0.0f;
 #pragma unroll
                 for (int u = 0; u < L::vWords; u++) vw[j][u] = seen(j) ? vw[j][u] : 0u;
@@ -428,19 +436,16 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
         // O^T: a column of V at a time
         repeat<L::vLoads>([&](auto y) {
             repeat<L::v_cols(y)>([&](auto e) {
-                constexpr int per = 32 / L::kBits, word = L::v_word_first(y) + e / per;
+                constexpr int per = 32 / L::kBits, word = L::v_word_first(y) + e / per, col = L::v_first(y) + e;
                 const bf16x8 a = operand(value_pair<STORE, e % per>(vw[0][word], vw[1][word]), value_pair<STORE, e % per>(vw[2][word], vw[3][word]),
                                          value_pair<STORE, e % per>(vw[4][word], vw[5][word]), value_pair<STORE, e % per>(vw[6][word], vw[7][word]));
-                constexpr int col = L::v_first(y) + e;
                 f32x4& o = acc[col];
 #pragma unroll
                 for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[k], o, 0, 0, 0);
             });
         });
-        if constexpr (more) {
-            load_values(next);
-            tile = next;
-        }
+        load_values(next);
+        tile = next;
     };
     if (count > 0) {
         find_pages(0);
@@ -461,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
             }
             arrived(q[0][s]);
         }
-        for (int i = 0; i + 1 < count; i++) step(i, std::true_type{});
-        step(count - 1, std::false_type{});
+        for (int i = 0; i < count; i++) step(i);
     }
     if (fresh) m = kNothing;
     l += __shfl_xor(l, 16, 64);
@@ -514,10 +518,10 @@ hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
     const bool wide = !p.q_bf16 || !p.y_bf16;
     const int64_t units = (int64_t)p.c.kv_heads * ((p.share + kHeadTile - 1) / kHeadTile);
     int64_t most = max_workgroups(kThreads) / (units * p.splits);
-    if (most > 65535) most = 65535;  // of a grid's third dimension
+    if (most > 65535) most = 65535;  // of a grid's second dimension
     for (int64_t first = 0; first < p.sequences; first += most) {
         const int64_t n = p.sequences - first < most ? p.sequences - first : most;
-        const dim3 grid((unsigned)p.splits, (unsigned)units, (unsigned)n);
+        const dim3 grid((unsigned)units, (unsigned)n, (unsigned)p.splits);
         auto with = [&](auto dim, auto scales) {
             constexpr int D = decltype(dim)::value, SCALES = decltype(scales)::value;
             if (wide) attend_kernel<STORE, SCALES, D, true><<<grid, kThreads, 0, s>>>(p, first);

@@ -40,15 +40,18 @@ struct SplitRange {
     FP4_HD int32_t used() const { return count > 0 ? (count - 1) / chunk + 1 : 0; }
     FP4_HD bool has(int32_t split) const { return (int64_t)split * chunk < count; }
 };
-// (`splits` as its logarithm: workgroups divide by it)
+// 2^split_log parts, or the largest power of two that leaves kPartLeast to each.  (Powers of two:
+// every workgroup divides by them.)
 FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log) {
     SplitRange r;
     r.begin = window > 0 && window < n ? n - window : 0;
     r.first = r.begin / kTilePositions * kTilePositions;
     r.count = n - r.first;
+    const int32_t fit = r.count < 2 * kPartLeast ? 0 : 31 - __builtin_clz((unsigned)(r.count / kPartLeast));
+    const int32_t log = fit < split_log ? fit : split_log;
     constexpr int32_t step = kTilePositions * kAttendWaves;  // every wavefront gets as many tiles
-    const int32_t chunk = (int32_t)(((int64_t)r.count + (1 << split_log) - 1) >> split_log);
-    r.chunk = chunk < kPartLeast ? kPartLeast : (chunk + step - 1) / step * step;
+    const int32_t chunk = (int32_t)(((int64_t)r.count + (1 << log) - 1) >> log);
+    r.chunk = chunk < step ? step : (chunk + step - 1) / step * step;
     return r;
 }
 
