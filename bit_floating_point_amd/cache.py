@@ -160,7 +160,7 @@ def _heads(t, name, shape, cache):
     rows, heads, dim = shape
     if step != 1 or (head != dim and heads > 1):
         raise ValueError(f"the heads of {name} must lie side by side")
-    return ld if rows > 1 or ld > heads * dim else heads * dim
+    return ld if rows > 1 else heads * dim  # the stride of a single row means nothing
 
 
 def _table(t, cache):
@@ -172,7 +172,7 @@ def _table(t, cache):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("page_table must be row-major")
-    return rows, cols, (ld if rows > 1 or ld > cols else cols)
+    return rows, cols, (ld if rows > 1 else cols)
 
 
 def _list(t, name, count, dtype, cache):

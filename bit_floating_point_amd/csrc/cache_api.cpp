@@ -23,7 +23,7 @@ constexpr int64_t kMostHeads = 65536;
 fp4_status matrix(const char* name, const void* p, int64_t rows, int64_t ld, int64_t cols, int32_t type) {
     if (ld < cols) return report(FP4_ERR_INVALID_ARG, "leading dimension of %s below its columns", name);
     if (!below(rows, ld, 1ll << 60)) return report(FP4_ERR_UNSUPPORTED, "%s spans more than 2^60 elements", name);
-    if (!aligned(p, 16) || (ld * size_of(type)) % 16 != 0)
+    if (!aligned(p, 16) || ld % (16 / size_of(type)) != 0)
         return report(FP4_ERR_ALIGNMENT, "%s must be 16-byte aligned, its rows a multiple of 16 bytes apart", name);
     return FP4_OK;
 }
@@ -191,7 +191,7 @@ fp4_status fp4_attend(const fp4_kv_cache* cache, const fp4_attend_desc* d, void*
     if (d->heads < 1 || d->heads % p.c.kv_heads != 0) return report(FP4_ERR_INVALID_ARG, "heads must be a multiple of kv_heads (got %d)", d->heads);
     if (d->heads > kMostHeads) return report(FP4_ERR_UNSUPPORTED, "at most 65536 heads (got %d)", d->heads);
     if (d->max_length < 0 || d->window < 0) return report(FP4_ERR_INVALID_ARG, "max_length and window must not be negative");
-    if (!(d->scale > -3.0e38f && d->scale < 3.0e38f)) return report(FP4_ERR_INVALID_ARG, "scale must be finite");
+    if (!(d->scale > -2.0e38f && d->scale < 2.0e38f)) return report(FP4_ERR_INVALID_ARG, "scale must be below 2e38");
     if ((st = table_of(d->page_table, d->sequences, d->max_pages, d->ld_table, p.c, &p.capacity))) return st;
     const int64_t cols = (int64_t)d->heads * p.c.head_dim;
     if ((st = matrix("q", d->q, d->sequences, d->ldq, cols, d->q_dtype)) || (st = matrix("y", d->y, d->sequences, d->ldy, cols, d->y_dtype))) return st;

@@ -90,7 +90,7 @@ typedef struct {
     const int32_t* lengths;     /* int32 [sequences]: positions, the new token's among them */
     int64_t max_length;         /* no length is larger (a larger one counts as this)   */
     int64_t window;             /* only the last `window` positions are seen; 0: all   */
-    float scale;                /* factor of the products q k                          */
+    float scale;                /* factor of the products q k, |scale| < 2e38         */
     int32_t y_dtype;            /* FP4_BF16 or FP4_F32                                 */
     void* y;                    /* [sequences, heads * head_dim], leading dim ldy      */
     int64_t ldy;
