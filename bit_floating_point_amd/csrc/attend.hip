@@ -10,7 +10,7 @@ namespace fp4 {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kFewParts = 16;
+constexpr int kFewParts = 4;
 
 __device__ __forceinline__ float block_reduce(float v, float* part, bool largest) {
 #pragma unroll
