@@ -213,15 +213,22 @@ constexpr int least_waves(int store, int dim, bool wide) {
     return (dim == 256 && (bf16 || (wide && store != kStoreE2m1))) || (dim == 192 && bf16 && wide) ? 1 : 2;
 }
 
-// WIDE: q or y is f32, and its terms three.
-template <int STORE, int SCALES, int D, bool WIDE>
+// Whether a workgroup takes two tiles of query heads: keys and values are then read and converted once for
+// 32 heads (one tile / two: 64 sequences of 8192, 64 heads on one, E4M3 112 / 65 us, bf16 185 / 103, E2M1 64 / 47;
+// 16 of 4096, 20 heads on each of 3, E4M3 27 / 22).  Up to rows of 128 values and without the terms of f32
+// there are registers for it.
+constexpr bool two_tiles(int share, int dim, bool wide) { return share > kHeadTile && dim <= 128 && !wide; }
+
+// WIDE: q or y is f32, and its terms three.  T: tiles of query heads of a workgroup.
+template <int STORE, int SCALES, int D, bool WIDE, int T>
 __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_kernel(AttendParams p, int64_t first_sequence) {
     using L = Plan<STORE, D>;
+    constexpr int kHeads = T * kHeadTile;
     constexpr int kQTerms = WIDE ? 3 : 1, kPTerms = WIDE ? 3 : 2;
     constexpr int kRound = 8;  // heads whose parts are joined at a time
     constexpr int H = 2, J = 4 * H;  // halves of a tile, a lane's positions in it
     __shared__ float joined[kAttendWaves][kRound][D + 4];
-    __shared__ float2 stats[kAttendWaves][kHeadTile];
+    __shared__ float2 stats[kAttendWaves][kHeads];
 
     const CacheParams& c = p.c;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -229,12 +236,12 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     // Workgroup (kv head and tile of its query heads, sequence, part).  Workgroups go to the eight XCDs in turn:
     // with parts first, those that most sequences do not have would leave the same XCDs idle (33
     // sequences of 1000 positions: 17 against 9 us).
-    const uint32_t tiles = (uint32_t)(p.share + kHeadTile - 1) / kHeadTile;
+    const uint32_t tiles = (uint32_t)(p.share + kHeads - 1) / kHeads;
     const int split = (int)blockIdx.z, kv_head = (int)(tiles == 1 ? blockIdx.x : blockIdx.x / tiles);
     const int head_tile = (int)(blockIdx.x - (uint32_t)kv_head * tiles);
     const int64_t sequence = first_sequence + blockIdx.y;
-    const int heads = min(p.share - head_tile * kHeadTile, kHeadTile);  // of this tile
-    const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeadTile;
+    const int heads = min(p.share - head_tile * kHeads, kHeads);  // of this workgroup
+    const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeads;
 
     const int32_t length = __builtin_amdgcn_readfirstlane(max(0, min(p.lengths[sequence], p.capacity)));
     const SplitRange range = split_range(length, p.window, p.split_log);
@@ -252,19 +259,20 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
         v_all = *reinterpret_cast<const float*>(c.v_scales);
     }
 
-    // q of head n, in K's order of columns: loaded here, in terms once the first tile is on its way
-    bf16x8 q[kQTerms][L::kSteps];
-    Raw8 q_raw[WIDE ? L::kSteps : 1];
+    // q of heads n (, n + 16), in K's order of columns: loaded here, in terms once the first tile is on its way
+    bf16x8 q[T][kQTerms][L::kSteps];
+    Raw8 q_raw[T][WIDE ? L::kSteps : 1];
     const bool q_bf16 = !WIDE || p.q_bf16;
-    {
-        const int64_t row = sequence * p.ldq + (first_head + n) * D;
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+        const int64_t row = sequence * p.ldq + (first_head + t * kHeadTile + n) * D;
         repeat<L::kLoads>([&](auto x) {
             constexpr int first = L::k_first(x), steps = L::k_steps(x);
 #pragma unroll
             for (int i = 0; i < steps; i++) {
                 const int64_t col = row + first * 32 + g * 8 * steps + 8 * i;
                 uint4 a{}, b{};
-                if (n < heads) {
+                if (t * kHeadTile + n < heads) {
                     if (q_bf16) {
                         a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + col);
                     } else {
@@ -272,16 +280,16 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
                         b = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p.q) + col)[1];
                     }
                 }
-                if constexpr (WIDE) q_raw[first + i] = Raw8{a, b};
-                else q[0][first + i] = __builtin_bit_cast(bf16x8, a);
+                if constexpr (WIDE) q_raw[t][first + i] = Raw8{a, b};
+                else q[t][0][first + i] = __builtin_bit_cast(bf16x8, a);
             }
         });
     }
 
-    float m = 0.0f, l = 0.0f;
+    float m[T] = {}, l[T] = {};
     bool fresh = true;  // nothing was seen yet
-    f32x4 acc[L::kCols];
-    repeat<L::kCols>([&](auto j) { acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
+    f32x4 acc[T][L::kCols];
+    repeat<T * L::kCols>([&](auto j) { acc[j / L::kCols][j % L::kCols] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
 
     uint32_t kw[H][L::kWords], vw[J][L::vWords];  // the tile on its way
     RowScales<SCALES> ks, vs;
@@ -360,88 +368,105 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     // condition ends.)
     auto step = [&](int i) {
         // Z^T of every half
-        f32x4 z[H];
+        f32x4 z[T][H];
 #pragma unroll
-        for (int h = 0; h < H; h++) z[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int h = 0; h < T * H; h++) z[h / H][h % H] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < L::kSteps; s++)
 #pragma unroll
             for (int h = 0; h < H; h++) {
                 const bf16x8 a = key_operand<STORE>(kw[h] + s * L::kStepBytes / 4);
 #pragma unroll
-                for (int k = kQTerms - 1; k >= 0; k--) z[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[k][s], z[h], 0, 0, 0);
+                for (int t = 0; t < T; t++)
+#pragma unroll
+                    for (int k = kQTerms - 1; k >= 0; k--) z[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[t][k][s], z[t][h], 0, 0, 0);
             }
         // x = z - m
-        float x[J];
+        float x[T][J];
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            const float dot = z[j / 4][j % 4];
-            if constexpr (kRows) x[j] = ks.fma(j, dot * factor, -m);
-            else x[j] = __builtin_fmaf(dot, factor, -m);
-        }
+        for (int t = 0; t < T; t++)
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const float dot = z[t][j / 4][j % 4];
+                if constexpr (kRows) x[t][j] = ks.fma(j, dot * factor, -m[t]);
+                else x[t][j] = __builtin_fmaf(dot, factor, -m[t]);
+            }
         if (((i + 1) & (64 / H - 1)) == 0) find_pages(i + 1);
         const Tile next = tile_of(i + 1);
         load_keys(next);
         // What is not seen has no weight, whatever its rows and scales hold.  (It may call for a new
         // reference in vain.)
         uint32_t absent = 0;
-        float most = x[0];
+        float most = x[0][0];
 #pragma unroll
         for (int h = 0; h < H; h++) absent |= tile.high[h];
 #pragma unroll
-        for (int j = 1; j < J; j++) most = fmaxf(most, x[j]);
+        for (int j = 1; j < T * J; j++) most = fmaxf(most, x[j / J][j % J]);
         const bool whole = tile.t >= range.begin && tile.t + kTilePositions <= end && (absent & kAbsent) == 0;
         auto seen = [&](int j) {
             const int t = tile.t + 16 * (j / 4) + 4 * g + j % 4;
             return whole | ((t >= range.begin) & (t < end) & ((tile.high[j / 4] & kAbsent) == 0));
         };
         if (fresh | __any(most > kSlack)) {
-            float top = kNothing;
+            const bool first = fresh;
 #pragma unroll
-            for (int j = 0; j < J; j++) top = fmaxf(top, seen(j) ? x[j] : kNothing);
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            // m moves to the first tile's largest z that has any (it was 0 until then), then upwards
-            const bool none = __all(top <= kNothing);
-            top = none ? 0.0f : fresh ? top : fmaxf(top, 0.0f);
-            const float f = fresh ? 1.0f : power2(-top);
-            fresh &= none;
-            m += top;
-            l *= f;
-            repeat<L::kCols>([&](auto j) { acc[j] *= f; });
+            for (int t = 0; t < T; t++) {
+                float top = kNothing;
 #pragma unroll
-            for (int j = 0; j < J; j++) x[j] -= top;
+                for (int j = 0; j < J; j++) top = fmaxf(top, seen(j) ? x[t][j] : kNothing);
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                // m moves to the first tile's largest z that has any (it was 0 until then), then upwards
+                const bool none = __all(top <= kNothing);
+                top = none ? 0.0f : first ? top : fmaxf(top, 0.0f);
+                const float f = first ? 1.0f : power2(-top);
+                fresh &= none;
+                m[t] += top;
+                l[t] *= f;
+                repeat<L::kCols>([&](auto j) { acc[t][j] *= f; });
+#pragma unroll
+                for (int j = 0; j < J; j++) x[t][j] -= top;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < J; j++) x[j] = power2(x[j]);
+        for (int j = 0; j < T * J; j++) x[j / J][j % J] = power2(x[j / J][j % J]);
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < J; j++) x[j] = seen(j) ? x[j] : 0.0f;
+            for (int j = 0; j < T * J; j++) x[j / J][j % J] = seen(j % J) ? x[j / J][j % J] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            l += x[j];
-            if constexpr (kRows) x[j] = vs.fma(j, x[j], 0.0f);
-        }
+        for (int t = 0; t < T; t++)
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                l[t] += x[t][j];
+                if constexpr (kRows) x[t][j] = vs.fma(j, x[t][j], 0.0f);
+            }
         if (!whole) {
 #pragma unroll
             for (int j = 0; j < J; j++) {
-                if constexpr (kRows) x[j] = seen(j) ? x[j] : 0.0f;
+                if constexpr (kRows) {
+#pragma unroll
+                    for (int t = 0; t < T; t++) x[t][j] = seen(j) ? x[t][j] : 0.0f;
+                }
 #pragma unroll
                 for (int u = 0; u < L::vWords; u++) vw[j][u] = seen(j) ? vw[j][u] : 0u;
             }
         }
-        bf16x8 weight[kPTerms];
-        terms_of<kPTerms>(x, weight);
+        bf16x8 weight[T][kPTerms];
+#pragma unroll
+        for (int t = 0; t < T; t++) terms_of<kPTerms>(x[t], weight[t]);
         // O^T: a column of V at a time
         repeat<L::vLoads>([&](auto y) {
             repeat<L::v_cols(y)>([&](auto e) {
                 constexpr int per = 32 / L::kBits, word = L::v_word_first(y) + e / per, col = L::v_first(y) + e;
                 const bf16x8 a = operand(value_pair<STORE, e % per>(vw[0][word], vw[1][word]), value_pair<STORE, e % per>(vw[2][word], vw[3][word]),
                                          value_pair<STORE, e % per>(vw[4][word], vw[5][word]), value_pair<STORE, e % per>(vw[6][word], vw[7][word]));
-                f32x4& o = acc[col];
 #pragma unroll
-                for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[k], o, 0, 0, 0);
+                for (int t = 0; t < T; t++) {
+                    f32x4& o = acc[t][col];
+#pragma unroll
+                    for (int k = kPTerms - 1; k >= 0; k--) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, weight[t][k], o, 0, 0, 0);
+                }
             });
         });
         load_values(next);
@@ -454,60 +479,69 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
         load_values(tile);
         // q is waited for here, beside those: in the loop it would be waited for, with all loads, in every turn
 #pragma unroll
-        for (int s = 0; s < L::kSteps; s++) {
-            if constexpr (WIDE) {
-                float x[8];
-                if (q_bf16) raw8_to_float<true>(q_raw[s], x);
-                else raw8_to_float<false>(q_raw[s], x);
-                bf16x8 t[kQTerms];
-                terms_of<kQTerms>(x, t);
+        for (int t = 0; t < T; t++)
 #pragma unroll
-                for (int k = 0; k < kQTerms; k++) q[k][s] = t[k];
+            for (int s = 0; s < L::kSteps; s++) {
+                if constexpr (WIDE) {
+                    float x[8];
+                    if (q_bf16) raw8_to_float<true>(q_raw[t][s], x);
+                    else raw8_to_float<false>(q_raw[t][s], x);
+                    bf16x8 terms[kQTerms];
+                    terms_of<kQTerms>(x, terms);
+#pragma unroll
+                    for (int k = 0; k < kQTerms; k++) q[t][k][s] = terms[k];
+                }
+                arrived(q[t][0][s]);
             }
-            arrived(q[0][s]);
-        }
         for (int i = 0; i < count; i++) step(i);
     }
-    if (fresh) m = kNothing;
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-
     // The wavefronts' parts, joined: each scales its own O to the largest m (and over the sum, if this is the
     // only part), then they are added in order.  Lane (n, g) holds columns first * 16 + cols (4 g + i) + e.
-    if (g == 0) stats[wave][n] = make_float2(m, l);
-    __syncthreads();
-    float top = stats[0][n].x, sum = 0.0f;
 #pragma unroll
-    for (int v = 1; v < kAttendWaves; v++) top = fmaxf(top, stats[v][n].x);
-#pragma unroll
-    for (int v = 0; v < kAttendWaves; v++) sum = __builtin_fmaf(stats[v][n].y, power2(stats[v][n].x - top), sum);
-    const bool alone = range.count <= range.chunk;
-    float own = power2(m - top) * v_all;
-    if (alone) own *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t head = sequence * p.heads + first_head;  // of n = 0
-    if (wave == 0 && g == 0 && n < heads) {
-        if (!alone) *reinterpret_cast<float2*>(p.part_ml + ((head + n) * p.splits + split) * 2) = make_float2(top, sum);
-        else if (p.lse) p.lse[head + n] = log_sum(top, sum);
+    for (int t = 0; t < T; t++) {
+        if (fresh) m[t] = kNothing;
+        l[t] += __shfl_xor(l[t], 16, 64);
+        l[t] += __shfl_xor(l[t], 32, 64);
+        if (g == 0) stats[wave][t * kHeadTile + n] = make_float2(m[t], l[t]);
     }
-    for (int r = 0; r < heads; r += kRound) {
-        if (r > 0) __syncthreads();
-        if (n >= r && n < r + kRound) {
-            repeat<L::vLoads>([&](auto x) {
-                repeat<L::v_cols(x)>([&](auto e) {
-                    constexpr int cols = L::v_cols(x), first = L::v_first(x);
+    __syncthreads();
+    const bool alone = range.count <= range.chunk;
+    const int64_t head = sequence * p.heads + first_head;  // of n = 0
 #pragma unroll
-                    for (int i = 0; i < 4; i++) joined[wave][n - r][first * 16 + cols * (4 * g + i) + e] = acc[first + e][i] * own;
-                });
-            });
+    for (int t = 0; t < T; t++) {
+        const int at = t * kHeadTile + n;
+        float top = stats[0][at].x, sum = 0.0f;
+#pragma unroll
+        for (int v = 1; v < kAttendWaves; v++) top = fmaxf(top, stats[v][at].x);
+#pragma unroll
+        for (int v = 0; v < kAttendWaves; v++) sum = __builtin_fmaf(stats[v][at].y, power2(stats[v][at].x - top), sum);
+        float own = power2(m[t] - top) * v_all;
+        if (alone) own *= sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (wave == 0 && g == 0 && at < heads) {
+            if (!alone) *reinterpret_cast<float2*>(p.part_ml + ((head + at) * p.splits + split) * 2) = make_float2(top, sum);
+            else if (p.lse) p.lse[head + at] = log_sum(top, sum);
         }
-        __syncthreads();
-        for (int e = threadIdx.x * 4; e < min(heads - r, kRound) * D; e += kThreads * 4) {
-            const int row = e / D, col = e % D;
-            f32x4 o = *reinterpret_cast<const f32x4*>(&joined[0][row][col]);
+        const int last = min(heads, (t + 1) * kHeadTile);
+        for (int r = t * kHeadTile; r < last; r += kRound) {
+            if (r > 0) __syncthreads();
+            if (at >= r && at < r + kRound) {
+                repeat<L::vLoads>([&](auto x) {
+                    repeat<L::v_cols(x)>([&](auto e) {
+                        constexpr int cols = L::v_cols(x), first = L::v_first(x);
 #pragma unroll
-            for (int v = 1; v < kAttendWaves; v++) o += *reinterpret_cast<const f32x4*>(&joined[v][row][col]);
-            if (!alone) *reinterpret_cast<f32x4*>(p.part_o + ((head + r + row) * p.splits + split) * D + col) = o;
-            else put4(p.y, p.y_bf16, sequence * p.ldy + (first_head + r + row) * D + col, o);
+                        for (int i = 0; i < 4; i++) joined[wave][at - r][first * 16 + cols * (4 * g + i) + e] = acc[t][first + e][i] * own;
+                    });
+                });
+            }
+            __syncthreads();
+            for (int e = threadIdx.x * 4; e < min(last - r, kRound) * D; e += kThreads * 4) {
+                const int row = e / D, col = e % D;
+                f32x4 o = *reinterpret_cast<const f32x4*>(&joined[0][row][col]);
+#pragma unroll
+                for (int v = 1; v < kAttendWaves; v++) o += *reinterpret_cast<const f32x4*>(&joined[v][row][col]);
+                if (!alone) *reinterpret_cast<f32x4*>(p.part_o + ((head + r + row) * p.splits + split) * D + col) = o;
+                else put4(p.y, p.y_bf16, sequence * p.ldy + (first_head + r + row) * D + col, o);
+            }
         }
     }
 }
@@ -516,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
 template <int STORE>
 hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
     const bool wide = !p.q_bf16 || !p.y_bf16;
-    const int64_t units = (int64_t)p.c.kv_heads * ((p.share + kHeadTile - 1) / kHeadTile);
+    const int tiles = two_tiles(p.share, p.c.head_dim, wide) ? 2 : 1;
+    const int64_t units = (int64_t)p.c.kv_heads * ((p.share + tiles * kHeadTile - 1) / (tiles * kHeadTile));
     int64_t most = max_workgroups(kThreads) / (units * p.splits);
     if (most > 65535) most = 65535;  // of a grid's second dimension
     for (int64_t first = 0; first < p.sequences; first += most) {
@@ -524,8 +559,11 @@ hipError_t launch_parts(const AttendParams& p, hipStream_t s) {
         const dim3 grid((unsigned)units, (unsigned)n, (unsigned)p.splits);
         auto with = [&](auto dim, auto scales) {
             constexpr int D = decltype(dim)::value, SCALES = decltype(scales)::value;
-            if (wide) attend_kernel<STORE, SCALES, D, true><<<grid, kThreads, 0, s>>>(p, first);
-            else attend_kernel<STORE, SCALES, D, false><<<grid, kThreads, 0, s>>>(p, first);
+            if (wide) return attend_kernel<STORE, SCALES, D, true, 1><<<grid, kThreads, 0, s>>>(p, first);
+            if constexpr (two_tiles(kHeadTile + 1, D, false)) {
+                if (tiles == 2) return attend_kernel<STORE, SCALES, D, false, 2><<<grid, kThreads, 0, s>>>(p, first);
+            }
+            attend_kernel<STORE, SCALES, D, false, 1><<<grid, kThreads, 0, s>>>(p, first);
         };
         auto go = [&](auto dim) {
             if constexpr (STORE != kStoreBf16) {
