@@ -17,7 +17,14 @@
 //      the sum is free too: q is read in the same order).
 //   V: lane (n, g) reads the same few columns of its 8 positions, 16 lanes a whole row; pairs of positions
 //      are interleaved by byte permutes and converted two at a time.
-// Codes convert to bf16 exactly, scales of rows go into z and into the weights p = 2^(z - m).
+// Codes convert to bf16 exactly, scales of rows go into z and into the weights p = 2^(z - m), which are sums of
+// two or three bf16 terms: one would be off by 2^-9.
+//
+// Bounds.  Rows of 8 bits and more: reading the cache.  16 sequences of 4096 positions, 40 heads of 128, E4M3: 114 us, 6.1 TB/s; one of
+// 131072, 8 kv heads of 128, bf16: 86 us, 6.3 TB/s, a streaming read's rate.  E2M1 converts twice as many values a byte: 96
+// sequences of up to 8192 positions, 8 kv heads with 8 heads each, 92 us, 4.6 TB/s; vector instructions (215 a tile)
+// take 43% of the SIMDs' cycles and matrix instructions 18%, waiting for loads and the ragged end the rest.
+// Scales converted where they are used, scalar bases, no load that anything waits for but its use: 175 -> 92.
 #pragma once
 #include <type_traits>
 

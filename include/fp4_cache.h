@@ -109,11 +109,12 @@ size_t fp4_attend_workspace_size(int64_t sequences, int32_t heads, int32_t kv_he
  * K and V are what the cache's rows stand for.  Rows that are not seen may hold anything.
  * Sums, maxima and exponentials are binary32.  On the matrix cores K, V and q are exact (an f32 q
  * as three bf16 terms) and the weights e^(z - m) are sums of two bf16 terms, three where q or y is
- * f32 (within 2^-18 and 2^-25 of themselves).  Long sequences are split into parts that are
- * joined in order: the result does not depend on timing; which parts depends on the sizes and
- * on the sequence's own length.
- *   workspace  device scratch of at least fp4_attend_workspace_size() bytes; calls that may
- *              overlap in time need one each                                            */
+ * f32 (within 2^-18 and 2^-25 of themselves, as long as a weight times its row's scale is above
+ * 2^-100).  The products z, and the values of V times 2^8, must stay finite in binary32.  Long
+ * sequences are split into parts that are joined in order: the result does not depend on timing;
+ * which parts depends on the sizes and on the sequence's own length.
+ *   workspace  device scratch of at least fp4_attend_workspace_size() bytes, 16-byte aligned; what
+ *              it holds before does not matter.  Calls that may overlap in time need one each  */
 fp4_status fp4_attend(const fp4_kv_cache* cache, const fp4_attend_desc* d, void* workspace,
                       size_t ws_bytes, void* stream);
 
