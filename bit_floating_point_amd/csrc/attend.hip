@@ -2,7 +2,7 @@
 //
 // Join: O = sum_i 2^(m_i - M) O_i, over sum_i 2^(m_i - M) l_i, in the order of the parts, one
 // workgroup per sequence and query head.  Bound by reading the parts, which is little (4 bytes a
-// value, parts of 512 positions or more): 4 to 5 us beside the parts' kernel, most of it launch and three
+// value, parts of 256 positions or more): 4 to 5 us beside the parts' kernel, most of it launch and three
 // loads that wait for each other.  Sequences of one part have their result already.
 #include "attend_kernel.h"
 
@@ -40,7 +40,7 @@ __device__ __forceinline__ void put_joined(const AttendParams& p, int64_t unit, 
     if (p.lse && col == 0) p.lse[unit] = attend::log_sum(top, sum);
 }
 __device__ __forceinline__ SplitRange range_of(const AttendParams& p, int64_t sequence) {
-    return split_range(max(0, min(p.lengths[sequence], p.capacity)), p.window, p.split_log);
+    return split_range(max(0, min(p.lengths[sequence], p.capacity)), p.window, p.split_log, p.least_log);
 }
 __device__ __forceinline__ void add4(float4& a, const float4& v, float w) {
     a.x = __builtin_fmaf(v.x, w, a.x), a.y = __builtin_fmaf(v.y, w, a.y);

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, least_waves(STORE, D, WIDE)) attend_
     const int64_t first_head = (int64_t)kv_head * p.share + head_tile * kHeads;
 
     const int32_t length = __builtin_amdgcn_readfirstlane(max(0, min(p.lengths[sequence], p.capacity)));
-    const SplitRange range = split_range(length, p.window, p.split_log);
+    const SplitRange range = split_range(length, p.window, p.split_log, p.least_log);
     if (split > 0 && !range.has(split)) return;
     const int begin = range.first + split * range.chunk;
     const int end = length - begin < range.chunk ? length : begin + range.chunk;

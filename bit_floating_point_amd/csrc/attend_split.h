@@ -10,28 +10,39 @@ namespace fp4 {
 
 constexpr int kTilePositions = 32;  // positions that a wavefront takes at a time
 constexpr int kAttendWaves = 4;     // wavefronts of a workgroup, on tiles in turn
-// Positions of a part, at least (the last one aside).  Shorter parts mean more to join, longer ones idle compute
-// units.  256 / 512 / 1024: 1 sequence of 512, 32 kv heads: 10.1 / 7.0 / 7.0 us (256 needs a join); 33 sequences of up to 2999 with
-// a window of 1000: 12.0 / 13.2 / 14.3.
-constexpr int kPartLeast = 512;
+// Positions of a part, at least (the last one aside): 2^9, or 2^8 where all sequences and heads together are fewer workgroups than
+// compute units, as far as that fills these once.  Shorter parts mean more to join, longer ones idle compute units (parts of
+// 512 / of 256, us, 8 kv heads E4M3: 8 sequences of 1000 14.4 / 12.0, 1 of 8192 12.8 / 10.4, 1 of 2000 bf16 16.0 / 11.5; past the fill
+// 1 of 16384 14.3 / 15.2, 1 of 32768 22.3 / 25.1; with more units 64 of up to 700 16.7 / 19.6).
+constexpr int kPartLeastLog = 9, kPartLeastFewLog = 8;
+constexpr int64_t kFewUnits = 256;
 constexpr int kMostSplits = 256;  // threads of a join's workgroup
 // Four workgroups a compute unit.  1024 / 2048 / 4096, us: 16x4096 of 40 kv heads E4M3 113 / 131 / 150; 48x8192 of 8, 153 / 167 /
 // 186, E2M1 84 / 95 / 104; 1x131072 bf16 86 / 90 / 91; lengths up to 8192, 96 sequences: E2M1 92 / 98 / 102, E4M3 200 / 190 /
 // 194, bf16 341 / 330 / 337: even batches lose more by two than ragged ones gain.
 constexpr int64_t kWantedWorkgroups = 1024;
-constexpr int kHeadTile = 16;       // query heads of a workgroup
+constexpr int kHeadTile = 16;       // query heads of a tile: a workgroup takes one or two
 
 // positions that a sequence of up to `length` sees, from a multiple of a tile on
 inline int64_t most_seen(int64_t length, int64_t window) {
     return window > 0 && window < length - kTilePositions ? window + kTilePositions - 1 : length;
 }
 
-// Parts per sequence, a power of two: as many as bring the launch to kWantedWorkgroups, none of them
-// shorter than kPartLeast.  Grows with max_length.
+// sequences, kv heads and tiles of their query heads
+inline int64_t attend_units(int64_t sequences, int32_t heads, int32_t kv_heads) {
+    return sequences * kv_heads * ((heads / kv_heads + kHeadTile - 1) / kHeadTile);
+}
+inline int32_t part_least_log(int64_t units) { return units < kFewUnits ? kPartLeastFewLog : kPartLeastLog; }
+
+// Parts per sequence, a power of two: as many as bring the launch to kWantedWorkgroups with none shorter than
+// 2^kPartLeastLog, or to kFewUnits with none shorter than 2^kPartLeastFewLog.  Up to 2^kPartLeastLog positions are one part always: they
+// need no join (1 sequence of 512, 32 kv heads: 7.0 us, in two parts 10.1).  Grows with max_length.
 inline int32_t split_count(int64_t sequences, int32_t heads, int32_t kv_heads, int64_t max_length, int64_t window) {
-    const int64_t tiles = (heads / kv_heads + kHeadTile - 1) / kHeadTile;
-    const int64_t units = sequences * kv_heads * tiles;
-    const int64_t parts = (most_seen(max_length, window) + kPartLeast - 1) / kPartLeast;
+    const int64_t units = attend_units(sequences, heads, kv_heads), seen = most_seen(max_length, window);
+    if (seen <= 1 << kPartLeastLog) return 1;
+    int64_t parts = (seen + (1 << kPartLeastFewLog) - 1) >> kPartLeastFewLog;
+    const int64_t fill = (kFewUnits + units - 1) / units, longer = (parts + 1) / 2;
+    parts = parts < fill ? parts : fill > longer ? fill : longer;
     int64_t wanted = (kWantedWorkgroups + units - 1) / units;
     if (wanted > parts) wanted = parts;
     int32_t s = 1;
@@ -46,14 +57,14 @@ struct SplitRange {
     FP4_HD int32_t used() const { return count > 0 ? (count - 1) / chunk + 1 : 0; }
     FP4_HD bool has(int32_t split) const { return (int64_t)split * chunk < count; }
 };
-// 2^split_log parts, or the largest power of two that leaves kPartLeast to each.  (Powers of two:
+// 2^split_log parts, or the largest power of two that leaves 2^least_log positions to each.  (Powers of two:
 // every workgroup divides by them.)
-FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log) {
+FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log, int32_t least_log) {
     SplitRange r;
     r.begin = window > 0 && window < n ? n - window : 0;
     r.first = r.begin / kTilePositions * kTilePositions;
     r.count = n - r.first;
-    const int32_t fit = r.count < 2 * kPartLeast ? 0 : 31 - __builtin_clz((unsigned)(r.count / kPartLeast));
+    const int32_t pieces = r.count >> least_log, fit = pieces < 2 ? 0 : 31 - __builtin_clz((unsigned)pieces);
     const int32_t log = fit < split_log ? fit : split_log;
     constexpr int32_t step = kTilePositions * kAttendWaves;  // every wavefront gets as many tiles
     const int32_t chunk = (int32_t)(((int64_t)r.count + (1 << log) - 1) >> log);

@@ -203,6 +203,7 @@ fp4_status fp4_attend(const fp4_kv_cache* cache, const fp4_attend_desc* d, void*
     p.window = d->window < kMostPositions ? (int32_t)d->window : 0;
     p.splits = p.capacity ? split_count(d->sequences, d->heads, p.c.kv_heads, p.capacity, p.window) : 1;
     p.split_log = __builtin_ctz((unsigned)p.splits);
+    p.least_log = part_least_log(attend_units(d->sequences, d->heads, p.c.kv_heads));
     const int64_t values = d->sequences * d->heads * p.splits;
     if (p.splits > 1) {
         const size_t need = (size_t)(values * (p.c.head_dim + 2)) * sizeof(float);

@@ -62,7 +62,7 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t) {
     need(p.splits == 1 || (p.part_o && p.part_ml && aligned(p.part_o, 16)), "no workspace");
     // the device's parts fit those of the host, for the longest sequence and some others
     for (const int32_t n : {p.capacity, p.capacity / 2, p.capacity / 3}) {
-        const SplitRange r = split_range(n, p.window, p.split_log);
+        const SplitRange r = split_range(n, p.window, p.split_log, p.least_log);
         need(r.used() <= p.splits && r.first >= 0 && r.count >= 0 && r.count <= p.capacity, "more parts than there is room for");
     }
     ++g_launches;

@@ -44,7 +44,8 @@ static void check(int64_t sequences, int32_t heads, int32_t kv_heads, int32_t mo
     const int32_t splits = split_count(sequences, heads, kv_heads, most, window);
     need(splits >= 1 && splits <= kMostSplits, "splits", sequences, most, splits);
     need((splits & (splits - 1)) == 0, "power of two", sequences, most, splits);
-    const SplitRange r = split_range(n, window, __builtin_ctz(splits));
+    need(splits == 1 || most_seen(most, window) > 512, "short ones in one part", most, window, splits);
+    const SplitRange r = split_range(n, window, __builtin_ctz(splits), part_least_log(attend_units(sequences, heads, kv_heads)));
     const int32_t parts = r.used();
     const int32_t begin = window > 0 && window < n ? n - window : 0;
     need(r.begin == begin && r.first <= begin && begin - r.first < kTilePositions && r.first % kTilePositions == 0, "begin", n, window, r.first);
