@@ -237,7 +237,8 @@ def fp4_attend(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, length
     the products (head_dim ** -0.5); window: the last so many positions only; max_length: no length is larger (the page
     table's, unless given: a smaller one saves launching parts that have no positions).  Returns y of q's shape (q's dtype
     unless y or y_dtype is given); a sequence that sees nothing has zeros.  lse (f32 [sequences, heads]) takes the logarithms of
-    the sums of exponentials.  A drafted token is a sequence of its own with the same row of the table."""
+    the sums of exponentials.  workspace: device memory that is used if it is large enough (else the call makes its own); calls
+    that may overlap in time need one each.  A drafted token is a sequence of its own with the same row of the table."""
     shape, dim = q.shape, cache.head_dim
     if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"q must be [sequences, heads, {dim}]")
