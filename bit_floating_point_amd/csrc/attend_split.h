@@ -23,9 +23,11 @@ constexpr int kMostSplits = 256;  // threads of a join's workgroup
 constexpr int64_t kWantedWorkgroups = 1024;
 constexpr int kHeadTile = 16;       // query heads of a tile: a workgroup takes one or two
 
-// positions that a sequence of up to `length` sees, from a multiple of a tile on
+// Positions that a sequence of up to `length` sees, from a multiple of a tile on: no more than the window and what lies
+// before it in its first tile.
 inline int64_t most_seen(int64_t length, int64_t window) {
-    return window > 0 && window < length - kTilePositions ? window + kTilePositions - 1 : length;
+    constexpr int64_t before = kTilePositions - 1;
+    return window > 0 && window < length - before ? window + before : length;
 }
 
 // sequences, kv heads and tiles of their query heads
