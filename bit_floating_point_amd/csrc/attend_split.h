@@ -34,21 +34,36 @@ inline int64_t most_seen(int64_t length, int64_t window) {
 inline int64_t attend_units(int64_t sequences, int32_t heads, int32_t kv_heads) {
     return sequences * kv_heads * ((heads / kv_heads + kHeadTile - 1) / kHeadTile);
 }
-inline int32_t part_least_log(int64_t units) { return units < kFewUnits ? kPartLeastFewLog : kPartLeastLog; }
 
-// Parts per sequence, a power of two: as many as bring the launch to kWantedWorkgroups with none shorter than
-// 2^kPartLeastLog, or to kFewUnits with none shorter than 2^kPartLeastFewLog.  Up to 2^kPartLeastLog positions are one part always: they
-// need no join (1 sequence of 512, 32 kv heads: 7.0 us, in two parts 10.1).  Grows with max_length.
+// How many parts a sequence gets: a power of two, as every workgroup divides by it.  One rule for the host, which makes room by the
+// longest sequence that a call can have, and for the device, which goes by each sequence's own length: the room is what the
+// longest one uses, and a sequence's parts are the same in every call that has as many units.
+struct PartRule {
+    int32_t few_log;  // up to 2^few_log parts may be as short as 2^kPartLeastFewLog
+    // log2 of the parts of a sequence that sees `count` positions.  Up to 2^kPartLeastLog positions are one part always: they
+    // need no join (1 sequence of 512, 32 kv heads: 7.0 us, in two parts 10.1).
+    FP4_HD int32_t parts_log(int32_t count) const {
+        if (count <= 1 << kPartLeastLog) return 0;
+        const int32_t size = 31 - __builtin_clz((unsigned)count);
+        const int32_t fit = size - kPartLeastFewLog, few = fit < few_log ? fit : few_log, more = size - kPartLeastLog;
+        return few > more ? few : more;
+    }
+};
+// the rule of a launch: short parts up to the first power of two that fills the compute units
+inline PartRule part_least_log(int64_t units) {
+    PartRule r{0};
+    while (units << r.few_log < kFewUnits) r.few_log++;
+    return r;
+}
+
+// Parts that a launch makes room for per sequence, a power of two: those of the longest sequence, as far as they bring it to
+// kWantedWorkgroups.  Grows with max_length (at most 2^30).
 inline int32_t split_count(int64_t sequences, int32_t heads, int32_t kv_heads, int64_t max_length, int64_t window) {
-    const int64_t units = attend_units(sequences, heads, kv_heads), seen = most_seen(max_length, window);
-    if (seen <= 1 << kPartLeastLog) return 1;
-    int64_t parts = (seen + (1 << kPartLeastFewLog) - 1) >> kPartLeastFewLog;
-    const int64_t fill = (kFewUnits + units - 1) / units, longer = (parts + 1) / 2;
-    parts = parts < fill ? parts : fill > longer ? fill : longer;
-    int64_t wanted = (kWantedWorkgroups + units - 1) / units;
-    if (wanted > parts) wanted = parts;
+    const int64_t units = attend_units(sequences, heads, kv_heads);
+    const int64_t parts = (int64_t)1 << part_least_log(units).parts_log((int32_t)most_seen(max_length, window));
+    const int64_t wanted = (kWantedWorkgroups + units - 1) / units;
     int32_t s = 1;
-    while (s < wanted && s < kMostSplits) s *= 2;
+    while (s < wanted && s < parts && s < kMostSplits) s *= 2;
     return s;
 }
 
@@ -59,15 +74,13 @@ struct SplitRange {
     FP4_HD int32_t used() const { return count > 0 ? (count - 1) / chunk + 1 : 0; }
     FP4_HD bool has(int32_t split) const { return (int64_t)split * chunk < count; }
 };
-// 2^split_log parts, or the largest power of two that leaves 2^least_log positions to each.  (Powers of two:
-// every workgroup divides by them.)
-FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log, int32_t least_log) {
+// the sequence's parts by the rule, 2^split_log at most
+FP4_HD inline SplitRange split_range(int32_t n, int32_t window, int32_t split_log, PartRule rule) {
     SplitRange r;
     r.begin = window > 0 && window < n ? n - window : 0;
     r.first = r.begin / kTilePositions * kTilePositions;
     r.count = n - r.first;
-    const int32_t pieces = r.count >> least_log, fit = pieces < 2 ? 0 : 31 - __builtin_clz((unsigned)pieces);
-    const int32_t log = fit < split_log ? fit : split_log;
+    const int32_t fit = rule.parts_log(r.count), log = fit < split_log ? fit : split_log;
     constexpr int32_t step = kTilePositions * kAttendWaves;  // every wavefront gets as many tiles
     const int32_t chunk = (int32_t)(((int64_t)r.count + (1 << log) - 1) >> log);
     r.chunk = chunk < step ? step : (chunk + step - 1) / step * step;

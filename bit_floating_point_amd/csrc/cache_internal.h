@@ -61,7 +61,8 @@ struct AttendParams {
     int64_t ldy;
     float* lse;
     int32_t splits;    // parts of a sequence, at most: a power of two
-    int32_t split_log, least_log;
+    int32_t split_log;
+    PartRule least_log;  // how short parts may be
     float* part_o;     // [sequences, heads, splits, head_dim], workspace
     float* part_ml;    // [sequences, heads, splits, 2]: maximum, sum
 };
