@@ -99,7 +99,8 @@ class KVCache:
     k, v: [pages, kv_heads, page_size, head_dim] bf16, or uint8 codes of `grid` (E2M1 packed: head_dim / 2 bytes
     a row), in any order of strides that keeps a row contiguous (the same for both).  Codes have scales: with
     g = gran("row") one a row, f32 or f16 [pages, kv_heads, page_size] contiguous; with g = gran("tensor") one
-    f32 value each, given.  The object keeps the tensors; make it once and use it for every call."""
+    f32 value each, given.  The object keeps the tensors; make it once and use it for every call.  Its descriptor holds
+    their addresses, so its fields are set once: for other tensors make a new object."""
     __slots__ = ("k", "v", "k_scales", "v_scales", "grid", "gran", "head_dim", "kv_heads", "page_size", "device", "index", "desc")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
@@ -129,6 +130,14 @@ class KVCache:
             k.data_ptr(), v.data_ptr(), pages, *strides[:3], heads, size, self.head_dim, L.FP4_BF16 if grid is None else L.FP4_PACKED,
             grid if grid is not None else L.fp4_grid(), g, k_scales.data_ptr() if k_scales is not None else None,
             v_scales.data_ptr() if v_scales is not None else None)
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError(f"{name} of a cache cannot be replaced: make a new KVCache")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a cache cannot be deleted: make a new KVCache")
 
 
 def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, grid: L.fp4_grid | None = None,
