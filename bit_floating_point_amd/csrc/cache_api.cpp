@@ -107,6 +107,14 @@ fp4_status cache_of(const fp4_kv_cache* cache, CacheParams* out) {
     return FP4_OK;
 }
 
+// Scales of rows that a write stores: keys' and values' share no memory.  (Rows span less than 2^61 bytes, 32 or more each.)
+fp4_status scales_apart(const CacheParams& c) {
+    if (c.scales != kScaleRowF32 && c.scales != kScaleRowF16) return FP4_OK;
+    const uint64_t bytes = (((uint64_t)c.pages * (uint64_t)c.kv_heads) << c.page_log) * (c.scales == kScaleRowF16 ? 2 : 4);
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c.k_scales), v = reinterpret_cast<uintptr_t>(c.v_scales);
+    return (k < v ? v - k : k - v) < bytes ? report(FP4_ERR_INVALID_ARG, "k_scales and v_scales share memory") : FP4_OK;
+}
+
 // the page table's sizes; *capacity: positions that a sequence can have
 fp4_status table_of(const int32_t* table, int64_t sequences, int64_t max_pages, int64_t ld, const CacheParams& c, int32_t* capacity) {
     if (sequences < 0 || sequences > 0x7fffffff || max_pages < 0)
@@ -161,9 +169,10 @@ extern "C" {
 
 fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream) {
     CacheRowsParams p{};
-    const fp4_status st = rows_of(cache, d, &p);
+    fp4_status st = rows_of(cache, d, &p);
     if (st) return st;
     if (p.tokens == 0 || p.sequences == 0 || p.capacity == 0) return report_ok();  // no token has a row
+    if ((st = scales_apart(p.c))) return st;
     return report_hip(launch_cache_write(p, (hipStream_t)stream), "fp4_cache_write");
 }
 

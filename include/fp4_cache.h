@@ -68,7 +68,8 @@ typedef struct {
  * less than 2^-126 unless amax is 0 (f16 scales: rounded to binary16, at most its largest
  * number), or the given s; codes of fl32(x * fl32(1/s)) as fp4_quantize_pack.  bf16: rounded to
  * nearest.  Tokens without a row are skipped; all other rows of the cache stay as they are.  No
- * two tokens of a call may have one row: what it holds then is a mixture of theirs. */
+ * two tokens of a call may have one row: what it holds then is a mixture of theirs.  Scales per row of
+ * keys and of values may not share memory (one given scale may be both's). */
 fp4_status fp4_cache_write(const fp4_kv_cache* cache, const fp4_cache_rows_desc* d, void* stream);
 
 /* ---- rows out of the cache ------------------------------------------------------- */
