@@ -247,7 +247,10 @@ def fp4_attend(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, length
     table's, unless given: a smaller one saves launching parts that have no positions).  Returns y of q's shape (q's dtype
     unless y or y_dtype is given); a sequence that sees nothing has zeros.  lse (f32 [sequences, heads]) takes the logarithms of
     the sums of exponentials.  workspace: device memory that is used if it is large enough (else the call makes its own); calls
-    that may overlap in time need one each.  A drafted token is a sequence of its own with the same row of the table."""
+    that may overlap in time need one each.  A drafted token is a sequence of its own with the same row of the table.
+
+    Scores and sums are binary32: |scale| log2(e) times the sum of |q k| (codes of k, before their row's scale) and 2^8 times the sum of |v|
+    over a sequence's positions must stay finite, and |z| log2(e) below 1.5e38 (include/fp4_cache.h)."""
     shape, dim = q.shape, cache.head_dim
     if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"q must be [sequences, heads, {dim}]")

@@ -111,9 +111,14 @@ size_t fp4_attend_workspace_size(int64_t sequences, int32_t heads, int32_t kv_he
  * Sums, maxima and exponentials are binary32.  On the matrix cores K, V and q are exact (an f32 q
  * as three bf16 terms) and the weights e^(z - m) are sums of two bf16 terms, three where q or y is
  * f32 (within 2^-18 and 2^-25 of themselves, as long as a weight times its row's scale is above
- * 2^-100).  The products z, and the values of V times 2^8, must stay finite in binary32.  Long
- * sequences are split into parts that are joined in order: the result does not depend on timing;
- * which parts depends on the sizes and on the sequence's own length.
+ * 2^-100).  Long sequences are split into parts that are joined in order: the result does not depend
+ * on timing; which parts depends on the sizes and on the sequence's own length.
+ * Binary32 must hold, over the positions that a sequence sees:
+ *   |q_d K[t, d]| summed over d, K without its scale (|q_d| itself below 3.38e38);
+ *   that times |scale| log2 e, and with a given scale of K times that too;
+ *   z log2 e, which must stay below 1.5e38 in magnitude;
+ *   2^8 |V[t, d]| summed over t, and 2^8 times a row's scale of V: weights pass 1 by as much between two
+ *   moves of the running maximum, and the quotient is taken last.
  *   workspace  device scratch of at least fp4_attend_workspace_size() bytes, 16-byte aligned; what
  *              it holds before does not matter.  Calls that may overlap in time need one each  */
 fp4_status fp4_attend(const fp4_kv_cache* cache, const fp4_attend_desc* d, void* workspace,
