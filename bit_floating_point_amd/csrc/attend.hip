@@ -11,9 +11,9 @@ namespace fp4 {
 namespace {
 
 constexpr int kJoinThreads = 256;
-// Up to so many parts a head has a wavefront, else a workgroup (wavefront / workgroup, us of the whole call: 96 sequences of 1100, 64
-// heads, two parts: 50.6 / 55.9; 40 of 1500, two: 35.9 / 37.5; 4 of 4096, eight: 14.9 / 14.55; 1 of 8192, sixteen: 14.5 /
-// 13.3).
+// Up to so many parts a head has a wavefront, else a workgroup (wavefront / workgroup, us of the whole call.  Two parts: 96 sequences of
+// 1100, 64 heads, 50.6 / 55.9, 40 of 1500 35.9 / 37.5.  Four: 60 of 2100, 32 heads, 52.8 / 54.7, 40 of 2048, 64 heads, 38.0 / 39.4, but with
+// few heads 4 of 1024 9.6 / 9.1 and 1 of 2000 11.7 / 11.2.  Eight: 4 of 4096 14.9 / 14.55.  Sixteen: 1 of 8192 14.5 / 13.3).
 constexpr int kFewParts = 4;
 
 __device__ __forceinline__ float block_reduce(float v, float* part, bool largest) {

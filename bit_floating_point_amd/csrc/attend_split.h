@@ -12,14 +12,17 @@ constexpr int kTilePositions = 32;  // positions that a wavefront takes at a tim
 constexpr int kAttendWaves = 4;     // wavefronts of a workgroup, on tiles in turn
 // Positions of a part, at least (the last one aside): 2^9, or 2^8 where all sequences and heads together are fewer workgroups than
 // compute units, as far as that fills these once.  Shorter parts mean more to join, longer ones idle compute units (parts of
-// 512 / of 256, us, 8 kv heads E4M3: 8 sequences of 1000 14.4 / 12.0, 1 of 8192 12.8 / 10.4, 1 of 2000 bf16 16.0 / 11.5; past the fill
-// 1 of 16384 14.3 / 15.2, 1 of 32768 22.3 / 25.1; with more units 64 of up to 700 16.7 / 19.6).
+// 512 / of 256, us of the call, 8 kv heads with 8 heads each, E4M3: 1 sequence of 8192 11.1 / 9.6, of 2048 10.8 / 9.1, 4 of 1024 10.5 / 9.6,
+// 1 of 2000 bf16 15.6 / 11.7; past the fill 1 of 16384 11.7 / 13.3, of 32768 18.7 / 21.8, 25 of 3000 38.0 / 39.6; with more
+// units 64 of up to 700 13.7 / 18.3).  Below 1024 positions one part, which has no join, is still a little quicker than two:
+// 8 of 1000 10.4 / 10.9, 2 of 800 9.1 / 10.0.
 constexpr int kPartLeastLog = 9, kPartLeastFewLog = 8;
 constexpr int64_t kFewUnits = 256;
 constexpr int kMostSplits = 256;  // threads of a join's workgroup
 // Four workgroups a compute unit.  1024 / 2048 / 4096, us: 16x4096 of 40 kv heads E4M3 113 / 131 / 150; 48x8192 of 8, 153 / 167 /
 // 186, E2M1 84 / 95 / 104; 1x131072 bf16 86 / 90 / 91; lengths up to 8192, 96 sequences: E2M1 92 / 98 / 102, E4M3 200 / 190 /
-// 194, bf16 341 / 330 / 337: even batches lose more by two than ragged ones gain.
+// 194, bf16 341 / 330 / 337: even batches lose more by two than ragged ones gain.  (Tiles of query heads are counted one by one:
+// a launch whose workgroups take two has half as many.)
 constexpr int64_t kWantedWorkgroups = 1024;
 constexpr int kHeadTile = 16;       // query heads of a tile: a workgroup takes one or two
 
